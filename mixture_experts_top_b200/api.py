@@ -57,6 +57,23 @@ _SIGNATURES = {
     "moe_expert_ffn_combine": (ctypes.c_int, [_c_p] * 11 + [ctypes.c_size_t, _c_p]),
     "moe_forward_combine_fused": (ctypes.c_int, [_c_p, _c_p]),
     "moe_forward": (ctypes.c_int, [_c_p] * 15 + [ctypes.c_size_t, _c_p]),
+    "moe_balance_workspace_size": (ctypes.c_size_t, [_c_p, ctypes.c_int32]),
+    "moe_balance_loss": (ctypes.c_int, [_c_p, ctypes.c_int32] + [_c_p] * 9
+                         + [ctypes.c_size_t, _c_p]),
+    "moe_balance_loss_backward": (ctypes.c_int, [_c_p, ctypes.c_int32] + [_c_p] * 8
+                                  + [ctypes.c_size_t, _c_p]),
+    "moe_route_backward_add": (ctypes.c_int, [_c_p] * 9 + [ctypes.c_int32] + [_c_p] * 6 +
+                               [ctypes.c_size_t, _c_p]),
+    "moe_dropout": (ctypes.c_int, [_c_p] * 2 + [ctypes.c_int32] * 2 + [_c_p] * 4),
+    "moe_combine_dropout": (ctypes.c_int, [_c_p] * 8),
+    "moe_combine_dropout_backward": (ctypes.c_int, [_c_p] * 9),
+    "moe_adapter_plan_size": (ctypes.c_size_t, [_c_p, ctypes.c_int32]),
+    "moe_adapter_plan": (ctypes.c_int, [_c_p, ctypes.c_int32, _c_p, _c_p, ctypes.c_size_t, _c_p]),
+    "moe_adapter": (ctypes.c_int, [_c_p] + [ctypes.c_int32] * 2 + [_c_p, ctypes.c_size_t]
+                    + [_c_p] * 8),
+    "moe_adapter_workspace_size": (ctypes.c_size_t, [_c_p] + [ctypes.c_int32] * 2),
+    "moe_adapter_backward": (ctypes.c_int, [_c_p] + [ctypes.c_int32] * 2
+                             + [_c_p, ctypes.c_size_t] + [_c_p] * 11 + [ctypes.c_size_t, _c_p]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_error_message": (ctypes.c_char_p, []),
 }
@@ -81,6 +98,12 @@ class MoeShard(ctypes.Structure):
     every rank's exchange record (world, 2E+1) int32."""
     _fields_ = [("rank", ctypes.c_int32), ("world", ctypes.c_int32), ("T_global", ctypes.c_int32),
                 ("records", ctypes.c_void_p)]
+
+
+class MoeDropout(ctypes.Structure):
+    """Mirror of ``moe_dropout_t``."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_dev", ctypes.c_void_p), ("token_base", ctypes.c_int64)]
 
 
 def make_config(T: int, d: int, d_hidden: int, d_out: int, E: int, top_k: int, kind: str,
@@ -348,3 +371,239 @@ def moe_forward(cfg, x, W_router, logit_bias, noise, W_in, W_up, W_out, output, 
         ctypes.byref(cfg), _ptr(x), _ptr(W_router), _ptr(logit_bias), _ptr(noise), _ptr(W_in),
         _ptr(W_up), _ptr(W_out), _ptr(output), _ptr(expert_indices), _ptr(gates), _ptr(aux_loss),
         _ptr(counts), _ptr(drop_mask), _ptr(ws), ws.numel(), _stream(stream)), "moe_forward")
+
+
+# ---- packed batches: balance loss per sequence, dropout, low-rank adapters ----
+#
+# These calls take many tensors of related shapes, so the binding checks each
+# one's type, shape and device before the library sees its pointer.
+
+def _arg(t, name: str, dtype, shape) -> Optional[int]:
+    """Pointer of a contiguous tensor of this type and shape on the current
+    device (shape None: any)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, name: str, dtype, shape) -> Optional[int]:
+    return None if t is None else _arg(t, name, dtype, shape)
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _buffer(t, name: str):
+    """Pointer and bytes of a workspace or plan (uint8)."""
+    import torch
+    return _arg(t, name, torch.uint8, None), t.numel()
+
+
+def _act(cfg):
+    import torch
+    return torch.bfloat16 if cfg.act_dtype == DTYPES["bf16"] else torch.float32
+
+
+def _seqs(seq_offsets):
+    """Number of sequences and the offsets' pointer (None: one sequence)."""
+    import torch
+    if seq_offsets is None:
+        return 1, None
+    if seq_offsets.dim() != 1:
+        raise ValueError("seq_offsets must have one dimension")
+    return seq_offsets.numel() - 1, _arg(seq_offsets, "seq_offsets", torch.int32, None)
+
+
+def _sized(n: int, where: str) -> int:
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, where,
+                       load_library().moe_last_error_message().decode())
+    return n
+
+
+def _alloc(n: int, device, stream):
+    import torch
+    buf = torch.empty(n, dtype=torch.uint8, device=device)
+    moe_workspace_init(buf, stream)
+    return buf
+
+
+def moe_balance_workspace_size(cfg: MoeConfig, n_seqs: int) -> int:
+    return _sized(load_library().moe_balance_workspace_size(ctypes.byref(cfg), int(n_seqs)),
+                  "moe_balance_workspace_size")
+
+
+def alloc_balance_workspace(cfg: MoeConfig, n_seqs: int, device="cuda", stream=None):
+    """Workspace of moe_balance_loss for n_seqs sequences, error word cleared."""
+    return _alloc(moe_balance_workspace_size(cfg, n_seqs), device, stream)
+
+
+def moe_balance_loss(cfg, seq_offsets, token_mask, logits, expert_indices, counts, prob_mean,
+                     tokens, losses, ws, stream=None) -> None:
+    """seq_offsets (n_seqs+1) int32 or None (one sequence: all tokens);
+    token_mask (T) uint8 or None; see include/moe.h for the outputs."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    n, off = _seqs(seq_offsets)
+    T, E = cfg.T, cfg.E
+    wp, wn = _buffer(ws, "ws")
+    _check(load_library().moe_balance_loss(
+        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,)),
+        _arg(logits, "logits", f32, (T, E)),
+        _arg(expert_indices, "expert_indices", i32, (T, cfg.top_k)),
+        _arg(counts, "counts", i32, (n, E)), _arg(prob_mean, "prob_mean", f32, (n, E)),
+        _arg(tokens, "tokens", i32, (n + 2,)), _arg(losses, "losses", f32, (2,)), wp, wn,
+        _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(cfg, seq_offsets, token_mask, logits, counts, tokens, dlosses,
+                              dlogits, ws, stream=None) -> None:
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    n, off = _seqs(seq_offsets)
+    T, E = cfg.T, cfg.E
+    wp, wn = _buffer(ws, "ws")
+    _check(load_library().moe_balance_loss_backward(
+        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,)),
+        _arg(logits, "logits", f32, (T, E)), _arg(counts, "counts", i32, (n, E)),
+        _arg(tokens, "tokens", i32, (n + 2,)), _arg(dlosses, "dlosses", f32, (2,)),
+        _arg(dlogits, "dlogits", f32, (T, E)), wp, wn, _stream(stream)),
+        "moe_balance_loss_backward")
+
+
+def moe_route_backward_add(cfg, x, W_router, logits, expert_indices, gates, f, dgates, daux,
+                           T_batch, dlogits_add, dx, dW_router, dbias, dlogits, ws,
+                           stream=None) -> None:
+    """moe_route_backward with dlogits_add (T, E) fp32 added to the logits' gradient."""
+    import torch
+    add = _arg(dlogits_add, "dlogits_add", torch.float32, (cfg.T, cfg.E))
+    _check(load_library().moe_route_backward_add(
+        ctypes.byref(cfg), _ptr(x), _ptr(W_router), _ptr(logits), _ptr(expert_indices),
+        _ptr(gates), _ptr(f), _ptr(dgates), _ptr(daux), int(T_batch), add, _ptr(dx),
+        _ptr(dW_router), _ptr(dbias), _ptr(dlogits), _ptr(ws), ws.numel(), _stream(stream)),
+        "moe_route_backward_add")
+
+
+def _drop(p, seed, offset, token_base):
+    """moe_dropout_t; offset is an int, or a one-element int64 CUDA tensor that
+    the kernel reads when it runs (fresh masks from one captured graph)."""
+    if isinstance(offset, int):
+        return MoeDropout(p, seed, offset, None, token_base)
+    import torch
+    return MoeDropout(p, seed, 0, _arg(offset, "offset", torch.int64, (1,)), token_base)
+
+
+def moe_dropout(cfg, p, seed, offset, token_base, x, add, out, stream=None) -> None:
+    """out = add + dropout(x) over (T, width) rows, bf16 or fp32; add may be
+    None, out may be x or add."""
+    import torch
+    dt, shape = x.dtype, x.shape
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"x must be bfloat16 or float32, got {dt}")
+    if len(shape) != 2 or shape[0] != cfg.T:
+        raise ValueError(f"x must have shape ({cfg.T}, width), got {tuple(shape)}")
+    d = _drop(p, seed, offset, token_base)
+    _check(load_library().moe_dropout(
+        ctypes.byref(cfg), ctypes.byref(d), shape[1],
+        DTYPES["bf16"] if dt is torch.bfloat16 else DTYPES["f32"], _arg(x, "x", dt, None),
+        _opt(add, "add", dt, shape), _arg(out, "out", dt, shape), _stream(stream)), "moe_dropout")
+
+
+def moe_combine_dropout(cfg, p, seed, offset, token_base, y_perm, dest, gates, residual, output,
+                        stream=None) -> None:
+    """moe_combine with dropout, plus residual (or None) added after it."""
+    import torch
+    act, T, k, w = _act(cfg), cfg.T, cfg.top_k, cfg.d_out
+    d = _drop(p, seed, offset, token_base)
+    _check(load_library().moe_combine_dropout(
+        ctypes.byref(cfg), ctypes.byref(d), _arg(y_perm, "y_perm", torch.float32, (T * k, w)),
+        _arg(dest, "dest", torch.int32, (T, k)), _arg(gates, "gates", torch.float32, (T, k)),
+        _opt(residual, "residual", act, (T, w)), _arg(output, "output", act, (T, w)),
+        _stream(stream)), "moe_combine_dropout")
+
+
+def moe_combine_dropout_backward(cfg, p, seed, offset, token_base, dy, y_perm, dest, gates,
+                                 dy_perm, dgates, stream=None) -> None:
+    import torch
+    f32, act, T, k, w = torch.float32, _act(cfg), cfg.T, cfg.top_k, cfg.d_out
+    d = _drop(p, seed, offset, token_base)
+    _check(load_library().moe_combine_dropout_backward(
+        ctypes.byref(cfg), ctypes.byref(d), _arg(dy, "dy", act, (T, w)),
+        _arg(y_perm, "y_perm", f32, (T * k, w)), _arg(dest, "dest", torch.int32, (T, k)),
+        _arg(gates, "gates", f32, (T, k)), _arg(dy_perm, "dy_perm", f32, (T * k, w)),
+        _arg(dgates, "dgates", f32, (T, k)), _stream(stream)), "moe_combine_dropout_backward")
+
+
+def moe_adapter_plan_size(cfg: MoeConfig, n_adapters: int) -> int:
+    return _sized(load_library().moe_adapter_plan_size(ctypes.byref(cfg), int(n_adapters)),
+                  "moe_adapter_plan_size")
+
+
+def moe_adapter_workspace_size(cfg: MoeConfig, n_adapters: int, rank: int) -> int:
+    return _sized(load_library().moe_adapter_workspace_size(ctypes.byref(cfg), int(n_adapters),
+                                                            int(rank)),
+                  "moe_adapter_workspace_size")
+
+
+def alloc_adapter_plan(cfg: MoeConfig, n_adapters: int, device="cuda", stream=None):
+    """Buffer of moe_adapter_plan, error word cleared."""
+    return _alloc(moe_adapter_plan_size(cfg, n_adapters), device, stream)
+
+
+def alloc_adapter_workspace(cfg: MoeConfig, n_adapters: int, rank: int, device="cuda"):
+    """Workspace of moe_adapter_backward."""
+    import torch
+    return torch.empty(moe_adapter_workspace_size(cfg, n_adapters, rank), dtype=torch.uint8,
+                       device=device)
+
+
+def moe_adapter_plan(cfg, n_adapters, token_adapter, plan, stream=None) -> None:
+    """Groups the tokens by adapter: token_adapter (T) int32, negative for none."""
+    import torch
+    pp, pn = _buffer(plan, "plan")
+    _check(load_library().moe_adapter_plan(
+        ctypes.byref(cfg), int(n_adapters),
+        _arg(token_adapter, "token_adapter", torch.int32, (cfg.T,)), pp, pn, _stream(stream)),
+        "moe_adapter_plan")
+
+
+def _adapter_shape(cfg, A):
+    if A.dim() != 3 or A.shape[1] != cfg.d:
+        raise ValueError(f"A must have shape (n_adapters, {cfg.d}, rank), got {tuple(A.shape)}")
+    return A.shape[0], A.shape[2]
+
+
+def moe_adapter(cfg, plan, x, A, B, scale, base, output, u, stream=None) -> None:
+    """output = base + scale x A B by each token's adapter; base and u may be None."""
+    import torch
+    bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
+    n, r = _adapter_shape(cfg, A)
+    pp, pn = _buffer(plan, "plan")
+    _check(load_library().moe_adapter(
+        ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d)), _arg(A, "A", bf, None),
+        _arg(B, "B", bf, (n, r, w)), _arg(scale, "scale", f32, (n,)),
+        _opt(base, "base", bf, (T, w)), _arg(output, "output", bf, (T, w)),
+        _opt(u, "u", f32, (T, r)), _stream(stream)), "moe_adapter")
+
+
+def moe_adapter_backward(cfg, plan, x, u, dy, A, B, scale, dx_add, dx, dA, dB, ws,
+                         stream=None) -> None:
+    import torch
+    bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
+    n, r = _adapter_shape(cfg, A)
+    pp, pn = _buffer(plan, "plan")
+    wp, wn = _buffer(ws, "ws")
+    _check(load_library().moe_adapter_backward(
+        ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d)), _arg(u, "u", f32, (T, r)),
+        _arg(dy, "dy", bf, (T, w)), _arg(A, "A", bf, None), _arg(B, "B", bf, (n, r, w)),
+        _arg(scale, "scale", f32, (n,)), _opt(dx_add, "dx_add", f32, (T, cfg.d)),
+        _arg(dx, "dx", f32, (T, cfg.d)), _arg(dA, "dA", f32, A.shape),
+        _arg(dB, "dB", f32, (n, r, w)), wp, wn, _stream(stream)), "moe_adapter_backward")

@@ -1,0 +1,858 @@
+// adapter.cu - low-rank adapters of many requests beside a projection that
+// all requests share (the routed layer itself), and their gradients.
+//
+// Token t carries an adapter a = token_adapter[t] (none if negative):
+//   u[t] = s_a x[t] A_a          output[t] = base[t] + u[t] B_a
+//   v[t] = s_a dy[t] B_a^T       dx[t] = dx_add[t] + v[t] A_a^T
+//   dA_a = sum_t x[t]^T v[t]     dB_a = sum_t u[t]^T dy[t]
+// with A_a (d, r), B_a (r, d_out), r <= 128: 2 r (d + d_out) products a token
+// against 2 (d + 2 d_out) bytes, so up to r = 64 or so HBM bounds it.
+//
+// plan     - the tokens grouped by adapter, in token order, and the row tiles
+//            of the groups.  One CTA per adapter counts all tokens in shared
+//            memory and writes its own rows: one launch, no global atomics.
+// low rank - both products of a row tile in one launch.  A cluster of CTAs
+//            shares a tile: each contracts its slice of the input's columns,
+//            the r-wide partial sums meet through distributed shared memory
+//            in CTA order, and each writes its slice of the output's columns;
+//            u never makes a trip through HBM between the products.
+// gradient - rows of an adapter on the contraction, 128 columns of x or dy a
+//            CTA; long adapters are split at fixed row positions and their
+//            parts added in order by a last launch.  No floating-point
+//            atomics anywhere.
+//
+// Precision: bf16 operands, fp32 sums.  The tensor core adds one staged block
+// at a time and the blocks are added in round-to-nearest fp32.  u and v are
+// fp32 values: where one is an operand it is split into bf16 terms, two
+// (16 bits) for the bf16 output, three (all 24 bits) for the fp32 gradients.
+#include "moe_device.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------- helpers --
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;   // 0: the 16 bytes are filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Byte offset of 16-byte piece c of row `row` in a tile of CPR pieces a row
+// (a power of two): the 8 rows a matrix load reads fall on distinct banks.
+template <int CPR>
+__device__ __forceinline__ uint32_t tile_at(int row, int c) {
+  constexpr int kPer = CPR >= 8 ? 1 : 8 / CPR;   // rows in 128 bytes
+  const int sw = (row / kPer) & (CPR >= 8 ? 7 : CPR - 1);
+  return (uint32_t)(row * CPR + (c ^ sw)) * 16u;
+}
+
+// A value as a sum of bf16 terms.
+template <int N>
+__device__ __forceinline__ void split_bf16(float v, __nv_bfloat16 (&t)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    t[i] = __float2bfloat16(v);
+    v -= __bfloat162float(t[i]);
+  }
+}
+
+// ------------------------------------------------------------------- plan --
+
+constexpr int kPlanThreads = 1024;
+
+// CTA g writes group g: adapter g's rows, or (g = n) the rows without one.
+__global__ void __launch_bounds__(kPlanThreads)
+    adapter_plan_kernel(const int32_t* __restrict__ ids, int T, int n, int TM, int32_t* header,
+                        int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
+                        int4* __restrict__ tiles, int32_t* err) {
+  pdl_wait_and_release();
+  __shared__ int32_t hist[kAdapterMaxCount + 1];
+  __shared__ int32_t wsum[32], wsum2[32];
+  __shared__ int32_t s_row0, s_tile0, s_run;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x;
+  auto group_of = [&](int t) {
+    const int a = __ldg(ids + t);
+    return a < 0 || a >= n ? n : a;
+  };
+  for (int i = tid; i <= n; i += kPlanThreads) hist[i] = 0;
+  __syncthreads();
+  for (int t0 = 0; t0 < T; t0 += kPlanThreads) {
+    const int t = t0 + tid;
+    const int a = t < T ? group_of(t) : -1;
+    // lanes of the same group add once
+    const unsigned peers = __match_any_sync(0xffffffffu, a);
+    if (a >= 0 && (peers & lanemask_lt()) == 0) atomicAdd(&hist[a], __popc(peers));
+    if (g == 0 && t < T && __ldg(ids + t) >= n) report_error(err, kDevBadExpertIndex);
+  }
+  __syncthreads();
+  // rows and tiles before group g
+  int r = 0, q = 0;
+  for (int i = tid; i < g; i += kPlanThreads) {
+    r += hist[i];
+    q += (hist[i] + TM - 1) / TM;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r += __shfl_xor_sync(0xffffffffu, r, o);
+    q += __shfl_xor_sync(0xffffffffu, q, o);
+  }
+  if (lane == 0) {
+    wsum[warp] = r;
+    wsum2[warp] = q;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    r = q = 0;
+    for (int w = 0; w < 32; ++w) {
+      r += wsum[w];
+      q += wsum2[w];
+    }
+    s_row0 = r;
+    s_tile0 = q;
+    s_run = 0;
+    offsets[g] = r;
+    if (g == n) {
+      offsets[n + 1] = T;
+      header[0] = T;
+      header[1] = n;
+      header[2] = q + (hist[n] + TM - 1) / TM;
+    }
+  }
+  __syncthreads();
+  const int row0 = s_row0, tile0 = s_tile0, cnt = hist[g];
+  for (int i = tid; i * TM < cnt; i += kPlanThreads)
+    tiles[tile0 + i] = make_int4(g, row0 + i * TM, min(TM, cnt - i * TM), 0);
+  for (int t0 = 0; t0 < T; t0 += kPlanThreads) {
+    const int t = t0 + tid;
+    const bool mine = t < T && group_of(t) == g;
+    const unsigned b = __ballot_sync(0xffffffffu, mine);
+    __syncthreads();   // the last block's wsum has been read
+    if (lane == 0) wsum[warp] = __popc(b);
+    __syncthreads();
+    const int v = wsum[lane];
+    int before = lane < warp ? v : 0, all = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (mine) rows[row0 + s_run + before + __popc(b & lanemask_lt())] = t;
+    __syncthreads();
+    if (tid == 0) s_run += all;
+  }
+}
+
+// --------------------------------------------------------------- low rank --
+
+template <int RP, int TM, bool BWD>
+struct LowRank {
+  static constexpr int KC = TM == 64 ? 64 : 128;      // input columns a stage
+  static constexpr int NC = TM == 64 ? 64 : 128;      // output columns a stage
+  static constexpr int WM = TM / 16;
+  static constexpr int WK = TM == 16 ? 8 : (RP == 16 ? 2 : 1);   // warps along the contraction
+  static constexpr int WN = 8 / (WM * WK);
+  static constexpr int NT = RP / 8 / WN;              // 8-wide tiles a warp, first product
+  static constexpr int W2 = 8 / WM;                   // warps along the output's columns
+  static constexpr int NT2 = NC / W2 / 8;
+  static constexpr int TERMS = BWD ? 3 : 2;
+  static constexpr int OB = BWD ? 4 : 2;              // bytes of an output element
+  static constexpr int S1 = TM * KC * 2 + KC * RP * 2;
+  static constexpr int S2 = RP * NC * 2 + TM * NC * OB;
+  static constexpr int ST1 = S1 > 24 * 1024 ? 3 : 4;
+  static constexpr int ST2 = 3;
+  static constexpr int RED = WK > 1 ? WK * TM * RP * 4 : 0;
+  static constexpr int RING0 = ST1 * S1 > ST2 * S2 ? ST1 * S1 : ST2 * S2;
+  static constexpr int RING = RING0 > RED ? RING0 : RED;
+  static constexpr int US = TERMS * TM * RP * 2;
+  static constexpr int PART = TM * RP * 4;
+  static constexpr int SMEM = RING + US + PART;
+};
+
+// in (T, K) bf16; W1, W2 per adapter: forward A (K, r) and B (r, N), backward
+// B (r, K) and A (N, r); base (T, N) and out (T, N): bf16 forward, fp32
+// backward; base may be null (0) or out.  u (T, r) fp32 or null.
+template <int RP, int TM, bool BWD>
+__global__ void __launch_bounds__(256)
+    low_rank_kernel(const __nv_bfloat16* __restrict__ in, const __nv_bfloat16* __restrict__ W1,
+                    const __nv_bfloat16* __restrict__ W2, const float* __restrict__ scale,
+                    const void* base, void* out, float* __restrict__ u, int T, int n, int r, int K,
+                    int N, const int32_t* __restrict__ header, const int32_t* __restrict__ rows,
+                    const int4* __restrict__ tiles, int32_t* err) {
+  using L = LowRank<RP, TM, BWD>;
+  pdl_wait_and_release();
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int32_t s_rows[TM];
+  const uint32_t ring = smem_u32(smem), us = ring + L::RING, part = us + L::US;
+  float* partp = reinterpret_cast<float*>(smem + L::RING + L::US);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t cs;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
+  const int CS = (int)cs, cr = (int)cluster_cta_rank();
+  const int tile = blockIdx.x / CS;
+  if (__ldg(header) != T || __ldg(header + 1) != n) {   // the same for every CTA
+    if (tid == 0) report_error(err, kDevBadPlan);
+    return;
+  }
+  if (tile >= __ldg(header + 2)) return;                // the same for the cluster
+  const int4 tl = __ldg(tiles + tile);
+  const int a = tl.x, nrows = tl.z;
+  if (tid < TM) s_rows[tid] = tid < nrows ? __ldg(rows + tl.y + tid) : -1;
+  __syncthreads();
+  const int nn = ceil_div_dev(N, L::NC);
+  const int n0 = (int)((long long)nn * cr / CS), n1 = (int)((long long)nn * (cr + 1) / CS);
+  if (a == n) {   // rows without an adapter: out = base
+    if (base == out) return;
+    constexpr int PV = 16 / L::OB;
+    const int v0 = n0 * L::NC / PV, v1 = min(n1 * L::NC, N) / PV, nv = v1 - v0;
+    for (int i = tid; i < nrows * nv; i += 256) {
+      const size_t at = (size_t)s_rows[i / nv] * (N / PV) + v0 + i % nv;
+      static_cast<uint4*>(out)[at] =
+          base != nullptr ? static_cast<const uint4*>(base)[at] : make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const __nv_bfloat16* w1 = W1 + (size_t)a * K * r;
+  const __nv_bfloat16* w2 = W2 + (size_t)a * N * r;
+
+  // ---- first product: part = in[rows, slice] W1[slice, :] ----
+  const int nk = ceil_div_dev(K, L::KC);
+  const int k0 = (int)((long long)nk * cr / CS), k1 = (int)((long long)nk * (cr + 1) / CS);
+  auto load1 = [&](int kc) {
+    const uint32_t xs = ring + (uint32_t)((kc - k0) % L::ST1) * L::S1;
+    const uint32_t ws = xs + TM * L::KC * 2;
+    constexpr int XC = L::KC / 8;
+#pragma unroll
+    for (int i = tid; i < TM * XC; i += 256) {
+      const int row = i / XC, c = i % XC, col = kc * L::KC + c * 8;
+      const int t = s_rows[row];
+      const bool ok = t >= 0 && col < K;
+      cp_async16(xs + tile_at<XC>(row, c), ok ? in + (size_t)t * K + col : in, ok);
+    }
+    if (!BWD) {   // [k][j]
+      constexpr int RC = RP / 8;
+#pragma unroll
+      for (int i = tid; i < L::KC * RC; i += 256) {
+        const int row = i / RC, c = i % RC, col = kc * L::KC + row;
+        const bool ok = col < K && c * 8 < r;
+        cp_async16(ws + tile_at<RC>(row, c), ok ? w1 + (size_t)col * r + c * 8 : w1, ok);
+      }
+    } else {      // [j][k]
+#pragma unroll
+      for (int i = tid; i < RP * XC; i += 256) {
+        const int row = i / XC, c = i % XC, col = kc * L::KC + c * 8;
+        const bool ok = row < r && col < K;
+        cp_async16(ws + tile_at<XC>(row, c), ok ? w1 + (size_t)row * K + col : w1, ok);
+      }
+    }
+  };
+  const int wm = warp % L::WM, wk = (warp / L::WM) % L::WK, wn = warp / (L::WM * L::WK);
+  float acc[L::NT][4];
+#pragma unroll
+  for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < L::ST1 - 1; ++i) {
+    if (k0 + i < k1) load1(k0 + i);
+    cp_commit();
+  }
+  for (int kc = k0; kc < k1; ++kc) {
+    cp_wait<L::ST1 - 2>();
+    __syncthreads();
+    if (kc + L::ST1 - 1 < k1) load1(kc + L::ST1 - 1);
+    cp_commit();
+    const uint32_t xs = ring + (uint32_t)((kc - k0) % L::ST1) * L::S1;
+    const uint32_t ws = xs + TM * L::KC * 2;
+    float c[L::NT][4];
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
+#pragma unroll
+    for (int ks = wk; ks < L::KC / 16; ks += L::WK) {
+      uint32_t fa[4];
+      ldsm4(xs + tile_at<L::KC / 8>(wm * 16 + (lane & 15), ks * 2 + (lane >> 4)), fa);
+#pragma unroll
+      for (int p = 0; p < L::NT / 2; ++p) {
+        const int j0 = wn * (RP / L::WN) + p * 16;
+        uint32_t fb[4];
+        if (!BWD)
+          ldsm4_t(ws + tile_at<RP / 8>(ks * 16 + (lane & 15), j0 / 8 + (lane >> 4)), fb);
+        else
+          ldsm4(ws + tile_at<L::KC / 8>(j0 + (lane & 7) + (lane >> 4) * 8,
+                                        ks * 2 + ((lane >> 3) & 1)), fb);
+        mma16816(c[2 * p], fa, fb[0], fb[1]);
+        mma16816(c[2 * p + 1], fa, fb[2], fb[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] += c[i][j];
+  }
+  cp_wait<0>();
+  __syncthreads();   // the ring is free
+
+  // ---- second product's loads ----
+  auto load2 = [&](int nc) {
+    const uint32_t ws = ring + (uint32_t)((nc - n0) % L::ST2) * L::S2;
+    const uint32_t bs = ws + RP * L::NC * 2;
+    if (!BWD) {   // [j][c]
+      constexpr int CC = L::NC / 8;
+#pragma unroll
+      for (int i = tid; i < RP * CC; i += 256) {
+        const int row = i / CC, c = i % CC, col = nc * L::NC + c * 8;
+        const bool ok = row < r && col < N;
+        cp_async16(ws + tile_at<CC>(row, c), ok ? w2 + (size_t)row * N + col : w2, ok);
+      }
+    } else {      // [c][j]
+      constexpr int RC = RP / 8;
+#pragma unroll
+      for (int i = tid; i < L::NC * RC; i += 256) {
+        const int row = i / RC, c = i % RC, col = nc * L::NC + row;
+        const bool ok = col < N && c * 8 < r;
+        cp_async16(ws + tile_at<RC>(row, c), ok ? w2 + (size_t)col * r + c * 8 : w2, ok);
+      }
+    }
+    constexpr int BC = L::NC * L::OB / 16;   // 16-byte pieces of a base row
+    constexpr int PV = 16 / L::OB;
+#pragma unroll
+    for (int i = tid; i < TM * BC; i += 256) {
+      const int row = i / BC, c = i % BC, col = nc * L::NC + c * PV;
+      const int t = s_rows[row];
+      const bool ok = t >= 0 && col < N && base != nullptr;
+      const uint8_t* src = static_cast<const uint8_t*>(base) + ((size_t)t * N + col) * L::OB;
+      cp_async16(bs + tile_at<BC>(row, c), ok ? src : reinterpret_cast<const uint8_t*>(w2), ok);
+    }
+  };
+  auto begin2 = [&]() {
+#pragma unroll
+    for (int i = 0; i < L::ST2 - 1; ++i) {
+      if (n0 + i < n1) load2(n0 + i);
+      cp_commit();
+    }
+  };
+
+  // ---- u: the warps' and then the CTAs' partial sums, in order ----
+  {
+    const int row = wm * 16 + (lane >> 2), col0 = wn * (RP / L::WN) + (lane & 3) * 2;
+    float* dst = L::WK > 1 ? reinterpret_cast<float*>(smem) + wk * TM * RP : partp;
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i) {
+      float* p = dst + row * RP + col0 + i * 8;
+      p[0] = acc[i][0];
+      p[1] = acc[i][1];
+      p[8 * RP] = acc[i][2];
+      p[8 * RP + 1] = acc[i][3];
+    }
+  }
+  if (L::WK > 1) {
+    __syncthreads();
+    for (int i = tid; i < TM * RP; i += 256) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < L::WK; ++w) v += reinterpret_cast<float*>(smem)[w * TM * RP + i];
+      partp[i] = v;
+    }
+    __syncthreads();
+  }
+  begin2();
+  if (CS > 1) cluster_sync_all();
+  else __syncthreads();
+  const float sc = __ldg(scale + a);
+  for (int i = tid * 4; i < TM * RP; i += 1024) {
+    const int row = i / RP, j = i % RP;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < CS; ++q) {
+      const float4 p = CS > 1 ? ld_cluster_f4(cluster_smem_addr(partp + i, (uint32_t)q))
+                              : *reinterpret_cast<const float4*>(partp + i);
+      v[0] += p.x;
+      v[1] += p.y;
+      v[2] += p.z;
+      v[3] += p.w;
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) v[m] *= sc;
+    const int t = s_rows[row];
+    if (u != nullptr && cr == 0 && t >= 0 && j < r)
+      *reinterpret_cast<float4*>(u + (size_t)t * r + j) = make_float4(v[0], v[1], v[2], v[3]);
+    __nv_bfloat16 tm[4][L::TERMS];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) split_bf16<L::TERMS>(v[m], tm[m]);
+#pragma unroll
+    for (int w = 0; w < L::TERMS; ++w) {
+      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(
+          smem + L::RING + w * TM * RP * 2 + tile_at<RP / 8>(row, j / 8) + (j % 8) * 2);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) p[m] = tm[m][w];
+    }
+  }
+  if (CS > 1) cluster_sync_all();   // peers have read this CTA's partial sums
+  else __syncthreads();
+
+  // ---- second product: out[rows, slice] = base + u W2[:, slice] ----
+  const int w2n = warp / L::WM;
+  constexpr int BC = L::NC * L::OB / 16;
+  for (int nc = n0; nc < n1; ++nc) {
+    cp_wait<L::ST2 - 2>();
+    __syncthreads();
+    if (nc + L::ST2 - 1 < n1) load2(nc + L::ST2 - 1);
+    cp_commit();
+    const uint32_t so = (uint32_t)((nc - n0) % L::ST2) * L::S2;
+    const uint32_t ws = ring + so;
+    float c[L::NT2][4];
+#pragma unroll
+    for (int i = 0; i < L::NT2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < RP / 16; ++ks) {
+      uint32_t fa[L::TERMS][4];
+#pragma unroll
+      for (int w = 0; w < L::TERMS; ++w)
+        ldsm4(us + w * TM * RP * 2 +
+                  tile_at<RP / 8>(wm * 16 + (lane & 15), ks * 2 + (lane >> 4)), fa[w]);
+#pragma unroll
+      for (int p = 0; p < L::NT2 / 2; ++p) {
+        const int cc = w2n * (L::NC / L::W2) + p * 16;
+        uint32_t fb[4];
+        if (!BWD)
+          ldsm4_t(ws + tile_at<L::NC / 8>(ks * 16 + (lane & 15), cc / 8 + (lane >> 4)), fb);
+        else
+          ldsm4(ws + tile_at<RP / 8>(cc + (lane & 7) + (lane >> 4) * 8,
+                                     ks * 2 + ((lane >> 3) & 1)), fb);
+#pragma unroll
+        for (int w = L::TERMS - 1; w >= 0; --w) {   // the small terms first
+          mma16816(c[2 * p], fa[w], fb[0], fb[1]);
+          mma16816(c[2 * p + 1], fa[w], fb[2], fb[3]);
+        }
+      }
+    }
+    uint8_t* bs = smem + so + RP * L::NC * 2;
+#pragma unroll
+    for (int i = 0; i < L::NT2; ++i) {
+      const int col = w2n * (L::NC / L::W2) + i * 8 + (lane & 3) * 2;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = wm * 16 + (lane >> 2) + h * 8, byte = col * L::OB;
+        uint8_t* p = bs + tile_at<BC>(row, byte / 16) + byte % 16;
+        if (!BWD) {
+          uint32_t* q = reinterpret_cast<uint32_t*>(p);
+          const uint32_t b = *q;
+          *q = pack_bf16x2(__uint_as_float(b << 16) + c[i][2 * h],
+                           __uint_as_float(b & 0xFFFF0000u) + c[i][2 * h + 1]);
+        } else {
+          float2* q = reinterpret_cast<float2*>(p);
+          const float2 b = *q;
+          *q = make_float2(b.x + c[i][2 * h], b.y + c[i][2 * h + 1]);
+        }
+      }
+    }
+    __syncthreads();
+    constexpr int PV = 16 / L::OB;
+#pragma unroll
+    for (int i = tid; i < TM * BC; i += 256) {
+      const int row = i / BC, cc = i % BC, col = nc * L::NC + cc * PV;
+      const int t = s_rows[row];
+      if (t >= 0 && col < N)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + ((size_t)t * N + col) * L::OB) =
+            *reinterpret_cast<const uint4*>(bs + tile_at<BC>(row, cc));
+    }
+  }
+  cp_wait<0>();
+}
+
+// --------------------------------------------------------------- gradient --
+
+constexpr int kGradCols = 128;   // columns of x (dA) or dy (dB) a CTA
+constexpr int kGradRows = 32;    // rows a stage
+
+template <int RP>
+struct Grad {
+  static constexpr int WN = RP >= 32 ? 2 : 1;
+  static constexpr int MT = WN;                    // 16-column tiles a warp (8 / WN warps along m)
+  static constexpr int NT = RP / 8 / WN;
+  static constexpr int XS = kGradRows * kGradCols * 2;
+  static constexpr int VS = kGradRows * RP * 4;
+  static constexpr int STAGE = XS + VS;
+  static constexpr int STAGES = 4;
+  static constexpr int TS = 3 * kGradRows * RP * 2;
+  static constexpr int SMEM = STAGES * STAGE + TS;
+};
+
+struct GradArgs {
+  const __nv_bfloat16* x;   // (T, d)
+  const __nv_bfloat16* dy;  // (T, d_out)
+  const float* u;           // (T, r)
+  const float* v;           // (T, r)
+  float* dA;                // (n, d, r)
+  float* dB;                // (n, r, d_out)
+  float* part;              // (slots, r (d + d_out)): parts of split adapters, dA's then dB's
+  const int32_t* header;
+  const int32_t* offsets;
+  const int32_t* rows;
+  int32_t* err;
+  int T, n, r, d, d_out, len;   // len: rows between split positions
+};
+
+// The adapter whose part has slot `slot` = (row block) + (adapter): the last
+// a with offsets[a] / len + a <= slot.
+__device__ __forceinline__ int find_adapter(const int32_t* __restrict__ offsets, int n, int len,
+                                            int slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;   // the answer + 1 is in (lo, hi]: adapter 0 always satisfies it
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const bool le = i < hi && __ldg(offsets + i) / len + i <= slot;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    if (c == 0) break;
+    hi = min(hi, lo + c * step);
+    lo = lo + (c - 1) * step + 1;
+  }
+  return lo - 1;
+}
+
+template <int RP>
+__global__ void __launch_bounds__(256) adapter_grad_kernel(GradArgs g) {
+  using L = Grad<RP>;
+  pdl_wait_and_release();
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t ring = smem_u32(smem), ts = ring + L::STAGES * L::STAGE;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (__ldg(g.header) != g.T || __ldg(g.header + 1) != g.n) {
+    if (tid == 0) report_error(g.err, kDevBadPlan);
+    return;
+  }
+  const int slot = blockIdx.y;
+  const int a = find_adapter(g.offsets, g.n, g.len, slot);
+  if (a < 0) return;
+  const int o0 = __ldg(g.offsets + a), o1 = __ldg(g.offsets + a + 1);
+  const long long blk = slot - a;
+  const int r0 = (int)max((long long)o0, blk * g.len);
+  const int r1 = (int)min((long long)o1, (blk + 1) * g.len);
+  if (r0 >= r1) return;
+  const bool whole = r0 == o0 && r1 == o1;   // the adapter's only part: straight to the gradient
+  const int mbx = ceil_div_dev(g.d, kGradCols);
+  const bool isA = (int)blockIdx.x < mbx;
+  const int m0 = (isA ? blockIdx.x : blockIdx.x - mbx) * kGradCols;
+  const int M = isA ? g.d : g.d_out, r = g.r;
+  const __nv_bfloat16* X = isA ? g.x : g.dy;
+  const float* V = isA ? g.v : g.u;
+  const int nst = ceil_div_dev(r1 - r0, kGradRows);
+  auto load = [&](int s) {
+    const uint32_t xs = ring + (uint32_t)(s % L::STAGES) * L::STAGE, vs = xs + L::XS;
+    constexpr int XC = kGradCols / 8, VC = RP / 4;
+#pragma unroll
+    for (int i = tid; i < kGradRows * XC; i += 256) {
+      const int row = i / XC, c = i % XC, col = m0 + c * 8, at = r0 + s * kGradRows + row;
+      const bool ok = at < r1 && col < M;
+      cp_async16(xs + tile_at<XC>(row, c), ok ? X + (size_t)__ldg(g.rows + at) * M + col : X, ok);
+    }
+#pragma unroll
+    for (int i = tid; i < kGradRows * VC; i += 256) {
+      const int row = i / VC, c = i % VC, at = r0 + s * kGradRows + row;
+      const bool ok = at < r1 && c * 4 < r;
+      cp_async16(vs + i * 16, ok ? V + (size_t)__ldg(g.rows + at) * r + c * 4 : V, ok);
+    }
+  };
+  const int wm = warp / L::WN, wn = warp % L::WN;
+  float acc[L::MT][L::NT][4];
+#pragma unroll
+  for (int m = 0; m < L::MT; ++m)
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < L::STAGES - 1; ++i) {
+    if (i < nst) load(i);
+    cp_commit();
+  }
+  for (int s = 0; s < nst; ++s) {
+    cp_wait<L::STAGES - 2>();
+    __syncthreads();
+    if (s + L::STAGES - 1 < nst) load(s + L::STAGES - 1);
+    cp_commit();
+    const uint32_t so = (uint32_t)(s % L::STAGES) * L::STAGE;
+    // the stage's v (or u) as three bf16 terms
+#pragma unroll
+    for (int i = tid; i < kGradRows * RP / 4; i += 256) {
+      const int row = i / (RP / 4), j = i % (RP / 4) * 4;
+      const float4 q = *reinterpret_cast<const float4*>(smem + so + L::XS + i * 16);
+      const float v[4] = {q.x, q.y, q.z, q.w};
+      __nv_bfloat16 t[4][3];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) split_bf16<3>(v[m], t[m]);
+#pragma unroll
+      for (int w = 0; w < 3; ++w) {
+        __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(
+            smem + L::STAGES * L::STAGE + w * kGradRows * RP * 2 + tile_at<RP / 8>(row, j / 8) +
+            (j % 8) * 2);
+        p[0] = __nv_bfloat162(t[0][w], t[1][w]);
+        p[1] = __nv_bfloat162(t[2][w], t[3][w]);
+      }
+    }
+    __syncthreads();
+    float c[L::MT][L::NT][4];
+#pragma unroll
+    for (int m = 0; m < L::MT; ++m)
+#pragma unroll
+      for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[m][i][j] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < kGradRows / 16; ++ks) {
+      uint32_t fa[L::MT][4];
+#pragma unroll
+      for (int m = 0; m < L::MT; ++m)
+        ldsm4_t(ring + so + tile_at<kGradCols / 8>(ks * 16 + (lane & 7) + (lane >> 4) * 8,
+                                                   (wm * L::MT + m) * 2 + ((lane >> 3) & 1)),
+                fa[m]);
+#pragma unroll
+      for (int w = 2; w >= 0; --w) {
+#pragma unroll
+        for (int p = 0; p < L::NT / 2; ++p) {
+          const int j0 = wn * (RP / L::WN) + p * 16;
+          uint32_t fb[4];
+          ldsm4_t(ts + w * kGradRows * RP * 2 +
+                      tile_at<RP / 8>(ks * 16 + (lane & 15), j0 / 8 + (lane >> 4)), fb);
+#pragma unroll
+          for (int m = 0; m < L::MT; ++m) {
+            mma16816(c[m][2 * p], fa[m], fb[0], fb[1]);
+            mma16816(c[m][2 * p + 1], fa[m], fb[2], fb[3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < L::MT; ++m)
+#pragma unroll
+      for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][i][j] += c[m][i][j];
+  }
+  cp_wait<0>();
+  const size_t dsz = (size_t)g.d * r, bsz = (size_t)g.d_out * r;
+  float* out = whole ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
+                     : g.part + (size_t)slot * (dsz + bsz) + (isA ? 0 : dsz);
+#pragma unroll
+  for (int m = 0; m < L::MT; ++m)
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i) {
+      const int j = wn * (RP / L::WN) + i * 8 + (lane & 3) * 2;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int mm = m0 + (wm * L::MT + m) * 16 + (lane >> 2) + h * 8;
+        if (mm >= M || j >= r) continue;
+        if (isA) {
+          *reinterpret_cast<float2*>(out + (size_t)mm * r + j) =
+              make_float2(acc[m][i][2 * h], acc[m][i][2 * h + 1]);
+        } else {
+          out[(size_t)j * M + mm] = acc[m][i][2 * h];
+          out[(size_t)(j + 1) * M + mm] = acc[m][i][2 * h + 1];
+        }
+      }
+    }
+}
+
+// Adapters in parts: the parts added in order; adapters without rows: zeros.
+__global__ void __launch_bounds__(256) adapter_reduce_kernel(GradArgs g) {
+  pdl_wait_and_release();
+  if (__ldg(g.header) != g.T || __ldg(g.header + 1) != g.n) return;
+  const int a = blockIdx.y;
+  const int o0 = __ldg(g.offsets + a), o1 = __ldg(g.offsets + a + 1);
+  const int b0 = o0 / g.len, b1 = o1 > o0 ? (o1 - 1) / g.len : b0 - 1;   // first and last block
+  if (b0 == b1) return;
+  const size_t dsz = (size_t)g.d * g.r, bsz = (size_t)g.d_out * g.r, all = dsz + bsz;
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all;
+       i += (size_t)gridDim.x * 1024) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = b0; b <= b1; ++b) {
+      const float4 p = *reinterpret_cast<const float4*>(g.part + (size_t)(b + a) * all + i);
+      s.x += p.x;
+      s.y += p.y;
+      s.z += p.z;
+      s.w += p.w;
+    }
+    float* dst = i < dsz ? g.dA + (size_t)a * dsz + i : g.dB + (size_t)a * bsz + (i - dsz);
+    *reinterpret_cast<float4*>(dst) = s;
+  }
+}
+
+int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+
+// Rows of a tile: 16 where there are few rows, in all or an adapter (decode),
+// so that they spread over the SMs and a tile is not mostly padding.
+int tile_rows(int T, int n) { return T <= 1024 || T <= 32 * n ? 16 : 64; }
+
+int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
+
+// Rows between the positions at which the gradient's contraction is split:
+// about four CTAs an SM, at least 256 rows.
+int grad_len(const moe_config_t& c) {
+  const int mb = ceil_div(c.d, kGradCols) + ceil_div(c.d_out, kGradCols);
+  const int parts = std::max(1, ceil_div(4 * 148, mb));
+  return std::max(256, ceil_div(ceil_div(c.T, parts), kGradRows) * kGradRows);
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+AdapterPlanLayout adapter_plan_layout(const moe_config_t& c, int n) {
+  AdapterPlanLayout L{};
+  L.ctrl = 0;
+  L.header = 64;   // cleared by moe_workspace_init: a plan not made fits no call
+  L.offsets = 256;
+  L.rows = L.offsets + up256((size_t)(n + 2) * 4);
+  L.tiles = L.rows + up256((size_t)c.T * 4);
+  L.total = L.tiles + up256((size_t)max_tiles(c.T, n) * 16);
+  return L;
+}
+
+AdapterWsLayout adapter_ws_layout(const moe_config_t& c, int n, int r) {
+  AdapterWsLayout L{};
+  const int len = grad_len(c);
+  L.v = 0;
+  L.part = up256((size_t)c.T * r * 4);
+  // an adapter needs parts only if its rows cross a split position
+  const size_t slots = c.T > len ? (size_t)(c.T / len + n + 1) : 0;
+  L.total = L.part + up256(slots * (size_t)r * ((size_t)c.d + c.d_out) * 4) + 256;
+  return L;
+}
+
+cudaError_t launch_adapter_plan(const moe_config_t& c, int n, const int32_t* ids, void* plan,
+                                cudaStream_t s) {
+  const AdapterPlanLayout L = adapter_plan_layout(c, n);
+  uint8_t* p = static_cast<uint8_t*>(plan);
+  return launch_kernel(adapter_plan_kernel, n + 1, kPlanThreads, 0, s, 0, ids, c.T, n,
+                       tile_rows(c.T, n), reinterpret_cast<int32_t*>(p + L.header),
+                       reinterpret_cast<int32_t*>(p + L.offsets),
+                       reinterpret_cast<int32_t*>(p + L.rows),
+                       reinterpret_cast<int4*>(p + L.tiles), reinterpret_cast<int32_t*>(p));
+}
+
+namespace {
+
+template <int RP, int TM, bool BWD>
+cudaError_t run_low_rank(const AdapterCall& a, cudaStream_t s) {
+  using L = LowRank<RP, TM, BWD>;
+  const AdapterPlanLayout P = adapter_plan_layout(*a.c, a.n);
+  uint8_t* p = static_cast<uint8_t*>(a.plan);
+  // CTAs of a tile's cluster: enough to give every SM about four
+  const int tiles = max_tiles(a.c->T, a.n);
+  const int most = std::min(ceil_div(a.K, L::KC), ceil_div(a.N, L::NC));
+  int cs = 1;
+  while (cs < 8 && cs * 2 <= most && tiles * cs < 4 * device_sm_count()) cs *= 2;
+  const auto kern = low_rank_kernel<RP, TM, BWD>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, (unsigned)tiles * cs, 256, L::SMEM, s, cs, a.in, a.W1, a.W2, a.scale,
+                       a.base, a.out, a.u, a.c->T, a.n, a.r, a.K, a.N,
+                       reinterpret_cast<const int32_t*>(p + P.header),
+                       reinterpret_cast<const int32_t*>(p + P.rows),
+                       reinterpret_cast<const int4*>(p + P.tiles), reinterpret_cast<int32_t*>(p));
+}
+
+template <int RP, bool BWD>
+cudaError_t run_tm(const AdapterCall& a, cudaStream_t s) {
+  return tile_rows(a.c->T, a.n) == 16 ? run_low_rank<RP, 16, BWD>(a, s)
+                                      : run_low_rank<RP, 64, BWD>(a, s);
+}
+
+template <bool BWD>
+cudaError_t run_rank(const AdapterCall& a, cudaStream_t s) {
+  switch (rank_pad(a.r)) {
+    case 16: return run_tm<16, BWD>(a, s);
+    case 32: return run_tm<32, BWD>(a, s);
+    case 64: return run_tm<64, BWD>(a, s);
+    default: return run_tm<128, BWD>(a, s);
+  }
+}
+
+template <int RP>
+cudaError_t run_grad(const GradArgs& g, cudaStream_t s) {
+  const auto kern = adapter_grad_kernel<RP>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), Grad<RP>::SMEM);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(ceil_div(g.d, kGradCols) + ceil_div(g.d_out, kGradCols)),
+                  (unsigned)(g.T / g.len + g.n + 1));
+  return launch_kernel(kern, grid, 256, Grad<RP>::SMEM, s, 0, g);
+}
+
+}  // namespace
+
+cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s) {
+  if (a.c->T == 0) return cudaSuccess;
+  return backward ? run_rank<true>(a, s) : run_rank<false>(a, s);
+}
+
+cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan, const void* x,
+                                const float* u, const void* dy, float* dA, float* dB, void* ws,
+                                cudaStream_t s) {
+  const size_t dsz = (size_t)c.d * r * n * 4, bsz = (size_t)c.d_out * r * n * 4;
+  if (c.T == 0) {
+    cudaError_t e = cudaMemsetAsync(dA, 0, dsz, s);
+    return e == cudaSuccess ? cudaMemsetAsync(dB, 0, bsz, s) : e;
+  }
+  const AdapterPlanLayout P = adapter_plan_layout(c, n);
+  const AdapterWsLayout W = adapter_ws_layout(c, n, r);
+  uint8_t* p = static_cast<uint8_t*>(plan);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const GradArgs g{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(dy), u,
+                   reinterpret_cast<const float*>(w + W.v), dA, dB,
+                   reinterpret_cast<float*>(w + W.part),
+                   reinterpret_cast<const int32_t*>(p + P.header),
+                   reinterpret_cast<const int32_t*>(p + P.offsets),
+                   reinterpret_cast<const int32_t*>(p + P.rows), reinterpret_cast<int32_t*>(p),
+                   c.T, n, r, c.d, c.d_out, grad_len(c)};
+  cudaError_t e;
+  switch (rank_pad(r)) {
+    case 16: e = run_grad<16>(g, s); break;
+    case 32: e = run_grad<32>(g, s); break;
+    case 64: e = run_grad<64>(g, s); break;
+    default: e = run_grad<128>(g, s); break;
+  }
+  if (e != cudaSuccess) return e;
+  const int per = std::max(1, std::min(ceil_div((c.d + c.d_out) * r, 1024),
+                                       ceil_div(8 * device_sm_count(), n)));
+  return launch_kernel(adapter_reduce_kernel, dim3((unsigned)per, (unsigned)n), 256, 0, s, 0, g);
+}
+
+}  // namespace moe

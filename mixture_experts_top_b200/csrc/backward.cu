@@ -98,12 +98,13 @@ __global__ void __launch_bounds__(256)
 
 constexpr int kQMax = 8;  // experts per lane (E <= 256)
 
-// One warp per token: the logit gradient of the gates and of aux.
+// One warp per token: the logit gradient of the gates and of aux, plus `add`
+// (T, E) where the caller has one of its own.
 __global__ void __launch_bounds__(256)
     route_dlogits_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                          const float* __restrict__ gates, const float* __restrict__ dgates,
                          const float* __restrict__ f, const float* __restrict__ daux, int T, int E,
-                         int k, double aux_scale, float* __restrict__ dlogits) {
+                         int k, double aux_scale, const float* add, float* dlogits) {
   pdl_wait_and_release();
   const int lane = threadIdx.x & 31;
   const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -169,10 +170,14 @@ __global__ void __launch_bounds__(256)
           if (e >> 5 == q) dl[q] += tj;
       }
     }
+    // add (or null) may be dlogits: the same thread reads and writes an element
     float* out = dlogits + (size_t)t * E;
 #pragma unroll
     for (int q = 0; q < kQMax; ++q)
-      if (lane + 32 * q < E) out[lane + 32 * q] = dl[q];
+      if (lane + 32 * q < E) {
+        if (add != nullptr) dl[q] += add[(size_t)t * E + lane + 32 * q];
+        out[lane + 32 * q] = dl[q];
+      }
   }
 }
 
@@ -519,7 +524,7 @@ cudaError_t launch_route_backward(const moe_config_t& c, const void* x, const fl
                                   const float* f, const float* dgates, const float* daux,
                                   int T_batch, float* dx, float* dW, float* dbias,
                                   float* dlogits, float* dw_part, float* dbias_part,
-                                  cudaStream_t s) {
+                                  cudaStream_t s, const float* dlogits_add) {
   const long long total = (long long)c.d * c.E;
   if (c.T == 0) {
     // no tokens: every gradient is zero
@@ -530,7 +535,7 @@ cudaError_t launch_route_backward(const moe_config_t& c, const void* x, const fl
   const int wblocks = std::min(ceil_div(c.T, 8), device_sm_count() * 16);
   cudaError_t e = launch_kernel(route_dlogits_kernel, wblocks, 256, 0, s, 0, logits, idx, gates,
                                 dgates, f, daux, c.T, c.E, c.top_k,
-                                (double)c.E / (double)T_batch, dlogits);
+                                (double)c.E / (double)T_batch, dlogits_add, dlogits);
   if (e != cudaSuccess) return e;
   const bool narrow = c.E <= 16;
   if (narrow && c.d % 8 == 0) {

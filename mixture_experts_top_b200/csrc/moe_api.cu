@@ -410,11 +410,13 @@ int moe_combine_backward(const moe_config_t* cfg, const void* dy, const void* y_
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_combine_backward");
 }
 
-int moe_route_backward(const moe_config_t* cfg, const void* x, const float* W_router,
-                       const float* logits, const int32_t* expert_indices, const float* gates,
-                       const float* f, const float* dgates, const float* daux, int32_t T_batch,
-                       float* dx, float* dW_router, float* dbias, float* dlogits, void* ws,
-                       size_t ws_bytes, moe_stream_t stream) {
+namespace {
+
+int route_backward_entry(const moe_config_t* cfg, const void* x, const float* W_router,
+                         const float* logits, const int32_t* expert_indices, const float* gates,
+                         const float* f, const float* dgates, const float* daux, int32_t T_batch,
+                         const float* dlogits_add, float* dx, float* dW_router, float* dbias, float* dlogits, void* ws,
+                         size_t ws_bytes, moe_stream_t stream, const char* name) {
   int st = check_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config_t& c = *cfg;
@@ -440,8 +442,32 @@ int moe_route_backward(const moe_config_t* cfg, const void* x, const float* W_ro
   const cudaError_t e = launch_route_backward(
       c, x, W_router, logits, expert_indices, gates, f, dgates, daux, Tb, dx, dW_router, dbias,
       dlogits != nullptr ? dlogits : at<float>(ws, L.dlogits), at<float>(ws, L.dw_part),
-      at<float>(ws, L.dbias_part), reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_route_backward");
+      at<float>(ws, L.dbias_part), reinterpret_cast<cudaStream_t>(stream), dlogits_add);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, name);
+}
+
+}  // namespace
+
+int moe_route_backward(const moe_config_t* cfg, const void* x, const float* W_router,
+                       const float* logits, const int32_t* expert_indices, const float* gates,
+                       const float* f, const float* dgates, const float* daux, int32_t T_batch,
+                       float* dx, float* dW_router, float* dbias, float* dlogits, void* ws,
+                       size_t ws_bytes, moe_stream_t stream) {
+  return route_backward_entry(cfg, x, W_router, logits, expert_indices, gates, f, dgates, daux,
+                              T_batch, nullptr, dx, dW_router, dbias, dlogits, ws, ws_bytes,
+                              stream, "moe_route_backward");
+}
+
+int moe_route_backward_add(const moe_config_t* cfg, const void* x, const float* W_router,
+                           const float* logits, const int32_t* expert_indices, const float* gates,
+                           const float* f, const float* dgates, const float* daux,
+                           int32_t T_batch, const float* dlogits_add, float* dx, float* dW_router,
+                           float* dbias, float* dlogits, void* ws, size_t ws_bytes,
+                           moe_stream_t stream) {
+  if (cfg != nullptr && cfg->T > 0) MOE_REQUIRE(dlogits_add);
+  return route_backward_entry(cfg, x, W_router, logits, expert_indices, gates, f, dgates, daux,
+                              T_batch, dlogits_add, dx, dW_router, dbias, dlogits, ws, ws_bytes,
+                              stream, "moe_route_backward_add");
 }
 
 size_t moe_expert_backward_workspace_size(const moe_config_t* cfg) {
@@ -550,6 +576,299 @@ int moe_permute_backward(const moe_config_t* cfg, const float* dx_perm, const in
   const cudaError_t e = launch_permute_backward(c, dx_perm, dest, dx_add, dx,
                                                 reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_permute_backward");
+}
+
+// ---- packed sequences: the balance loss per sequence ----
+
+namespace {
+
+int check_sized_ws(const void* ws, size_t ws_bytes, size_t need, const char* what) {
+  if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, std::string(what) + " is NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(MOE_ERR_WORKSPACE, std::string(what) + " must be 256-byte aligned");
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE,
+                std::string(what) + " too small: need " + std::to_string(need) + " bytes");
+  return MOE_OK;
+}
+
+int check_balance(const moe_config_t* cfg, int32_t n_seqs, const int32_t* seq_offsets) {
+  const int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (n_seqs < 1) return fail(MOE_ERR_INVALID_ARG, "n_seqs must be >= 1");
+  if (seq_offsets == nullptr && n_seqs != 1)
+    return fail(MOE_ERR_INVALID_ARG, "seq_offsets is NULL (allowed for one sequence)");
+  if ((int64_t)cfg->T * cfg->top_k > (int64_t)1 << 30 || n_seqs > 1 << 30)
+    return fail(MOE_ERR_UNSUPPORTED, "balance loss: T * top_k and n_seqs must be <= 2^30");
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_balance_workspace_size(const moe_config_t* cfg, int32_t n_seqs) {
+  static const int32_t kAny = 0;   // the offsets are not part of the size
+  if (check_balance(cfg, n_seqs, &kAny) != MOE_OK) return 0;
+  return balance_layout(*cfg, n_seqs).total;
+}
+
+int moe_balance_loss(const moe_config_t* cfg, int32_t n_seqs, const int32_t* seq_offsets,
+                     const uint8_t* token_mask, const float* logits,
+                     const int32_t* expert_indices, int32_t* counts, float* prob_mean,
+                     int32_t* tokens, float* losses, void* ws, size_t ws_bytes,
+                     moe_stream_t stream) {
+  int st = check_balance(cfg, n_seqs, seq_offsets);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (c.T > 0) {
+    MOE_REQUIRE(logits);
+    MOE_REQUIRE(expert_indices);
+  }
+  MOE_REQUIRE(counts);
+  MOE_REQUIRE(prob_mean);
+  MOE_REQUIRE(tokens);
+  MOE_REQUIRE(losses);
+  if ((st = check_sized_ws(ws, ws_bytes, balance_layout(c, n_seqs).total, "workspace")) != MOE_OK)
+    return st;
+  const cudaError_t e = launch_balance_loss(c, n_seqs, seq_offsets, token_mask, logits,
+                                            expert_indices, counts, prob_mean, tokens, losses, ws,
+                                            reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_balance_loss");
+}
+
+int moe_balance_loss_backward(const moe_config_t* cfg, int32_t n_seqs, const int32_t* seq_offsets,
+                              const uint8_t* token_mask, const float* logits,
+                              const int32_t* counts, const int32_t* tokens, const float* dlosses,
+                              float* dlogits, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  int st = check_balance(cfg, n_seqs, seq_offsets);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (c.T > 0) {
+    MOE_REQUIRE(logits);
+    MOE_REQUIRE(dlogits);
+  }
+  MOE_REQUIRE(counts);
+  MOE_REQUIRE(tokens);
+  MOE_REQUIRE(dlosses);
+  if ((st = check_sized_ws(ws, ws_bytes, balance_layout(c, n_seqs).total, "workspace")) != MOE_OK)
+    return st;
+  const cudaError_t e = launch_balance_loss_backward(c, n_seqs, seq_offsets, token_mask, logits,
+                                                     counts, tokens, dlosses, dlogits, ws,
+                                                     reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_balance_loss_backward");
+}
+
+// ---- dropout ----
+
+namespace {
+
+// The kernel's form of `drop` for rows of `width` elements.
+int check_dropout(const moe_dropout_t* drop, int width, DropArgs* out) {
+  if (drop == nullptr) return fail(MOE_ERR_INVALID_ARG, "drop is NULL");
+  if (!(drop->p >= 0.0 && drop->p < 1.0))
+    return fail(MOE_ERR_INVALID_ARG, "p must be in [0, 1)");
+  const double thr = std::floor(drop->p * 65536.0 + 0.5);
+  if (thr > 65535.0)
+    return fail(MOE_ERR_INVALID_ARG, "p rounds to 1 in steps of 2^-16");
+  if (drop->token_base < 0) return fail(MOE_ERR_INVALID_ARG, "token_base must be >= 0");
+  if ((reinterpret_cast<uintptr_t>(drop->offset_dev) & 7u) != 0)
+    return fail(MOE_ERR_INVALID_ARG, "offset_dev must be 8-byte aligned");
+  out->thr = (uint32_t)thr;
+  out->scale = (float)(65536.0 / (65536.0 - thr));
+  out->seed = drop->seed;
+  out->offset = drop->offset;
+  out->offset_dev = drop->offset_dev;
+  out->block0 = (uint64_t)drop->token_base * (uint64_t)(width / 8);
+  return MOE_OK;
+}
+
+}  // namespace
+
+int moe_dropout(const moe_config_t* cfg, const moe_dropout_t* drop, int32_t width, int32_t dtype,
+                const void* x, const void* add, void* out, moe_stream_t stream) {
+  int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (!is_mult8(width)) return fail(MOE_ERR_UNSUPPORTED, "width must be a multiple of 8, >= 8");
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
+  DropArgs d;
+  if ((st = check_dropout(drop, width, &d)) != MOE_OK) return st;
+  if (c.T > 0) {
+    MOE_REQUIRE(x);
+    MOE_REQUIRE(out);
+  }
+  MOE_ALIGNED16(x);
+  MOE_ALIGNED16(add);
+  MOE_ALIGNED16(out);
+  const cudaError_t e = launch_dropout(c.T, width, dtype == MOE_BF16, x, add, out, d,
+                                       reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_dropout");
+}
+
+int moe_combine_dropout(const moe_config_t* cfg, const moe_dropout_t* drop, const void* y_perm,
+                        const int32_t* dest, const float* gates, const void* residual,
+                        void* output, moe_stream_t stream) {
+  int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  DropArgs d;
+  if ((st = check_dropout(drop, c.d_out, &d)) != MOE_OK) return st;
+  if (c.T > 0) {
+    MOE_REQUIRE(y_perm);
+    MOE_REQUIRE(dest);
+    MOE_REQUIRE(gates);
+    MOE_REQUIRE(output);
+  }
+  MOE_ALIGNED16(y_perm);
+  MOE_ALIGNED16(residual);
+  MOE_ALIGNED16(output);
+  const cudaError_t e =
+      launch_combine_dropout(c, static_cast<const float*>(y_perm), dest, gates, residual, output,
+                             d, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_combine_dropout");
+}
+
+int moe_combine_dropout_backward(const moe_config_t* cfg, const moe_dropout_t* drop,
+                                 const void* dy, const void* y_perm, const int32_t* dest,
+                                 const float* gates, float* dy_perm, float* dgates,
+                                 moe_stream_t stream) {
+  int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  DropArgs d;
+  if ((st = check_dropout(drop, c.d_out, &d)) != MOE_OK) return st;
+  if (c.T > 0) {
+    MOE_REQUIRE(dy);
+    MOE_REQUIRE(y_perm);
+    MOE_REQUIRE(dest);
+    MOE_REQUIRE(gates);
+    MOE_REQUIRE(dy_perm);
+    MOE_REQUIRE(dgates);
+  }
+  MOE_ALIGNED16(dy);
+  MOE_ALIGNED16(y_perm);
+  MOE_ALIGNED16(dy_perm);
+  const cudaError_t e = launch_combine_dropout_backward(
+      c, dy, static_cast<const float*>(y_perm), dest, gates, dy_perm, dgates, d,
+      reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_combine_dropout_backward");
+}
+
+// ---- low-rank adapters ----
+
+namespace {
+
+int check_adapters(const moe_config_t* cfg, int32_t n, int32_t rank) {
+  const int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->act_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "adapters: bf16 activations only");
+  if (n < 1) return fail(MOE_ERR_INVALID_ARG, "n_adapters must be >= 1");
+  if (n > kAdapterMaxCount) return fail(MOE_ERR_UNSUPPORTED, "n_adapters > 1024 is not supported");
+  if (rank < 1) return fail(MOE_ERR_INVALID_ARG, "rank must be >= 1");
+  if (rank % 8 != 0 || rank > kAdapterMaxRank)
+    return fail(MOE_ERR_UNSUPPORTED, "rank must be a multiple of 8, at most 128");
+  if (cfg->T > 1 << 30) return fail(MOE_ERR_UNSUPPORTED, "adapters: T must be <= 2^30");
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_adapter_plan_size(const moe_config_t* cfg, int32_t n_adapters) {
+  if (check_adapters(cfg, n_adapters, 8) != MOE_OK) return 0;
+  return adapter_plan_layout(*cfg, n_adapters).total;
+}
+
+size_t moe_adapter_workspace_size(const moe_config_t* cfg, int32_t n_adapters, int32_t rank) {
+  if (check_adapters(cfg, n_adapters, rank) != MOE_OK) return 0;
+  return adapter_ws_layout(*cfg, n_adapters, rank).total;
+}
+
+int moe_adapter_plan(const moe_config_t* cfg, int32_t n_adapters, const int32_t* token_adapter,
+                     void* plan, size_t plan_bytes, moe_stream_t stream) {
+  int st = check_adapters(cfg, n_adapters, 8);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (c.T > 0) MOE_REQUIRE(token_adapter);
+  if ((st = check_sized_ws(plan, plan_bytes, adapter_plan_layout(c, n_adapters).total, "plan")) !=
+      MOE_OK)
+    return st;
+  const cudaError_t e = launch_adapter_plan(c, n_adapters, token_adapter, plan,
+                                            reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_adapter_plan");
+}
+
+int moe_adapter(const moe_config_t* cfg, int32_t n_adapters, int32_t rank, void* plan,
+                size_t plan_bytes, const void* x, const void* A, const void* B,
+                const float* scale, const void* base, void* output, float* u,
+                moe_stream_t stream) {
+  int st = check_adapters(cfg, n_adapters, rank);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (c.T > 0) {
+    MOE_REQUIRE(x);
+    MOE_REQUIRE(output);
+  }
+  MOE_REQUIRE(A);
+  MOE_REQUIRE(B);
+  MOE_REQUIRE(scale);
+  MOE_ALIGNED16(x);
+  MOE_ALIGNED16(A);
+  MOE_ALIGNED16(B);
+  MOE_ALIGNED16(base);
+  MOE_ALIGNED16(output);
+  MOE_ALIGNED16(u);
+  if ((st = check_sized_ws(plan, plan_bytes, adapter_plan_layout(c, n_adapters).total, "plan")) !=
+      MOE_OK)
+    return st;
+  const AdapterCall a{&c, n_adapters, rank, c.d, c.d_out, plan,
+                      static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(A),
+                      static_cast<const __nv_bfloat16*>(B), scale, base, output, u};
+  const cudaError_t e = launch_adapter(a, false, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_adapter");
+}
+
+int moe_adapter_backward(const moe_config_t* cfg, int32_t n_adapters, int32_t rank, void* plan,
+                         size_t plan_bytes, const void* x, const float* u, const void* dy,
+                         const void* A, const void* B, const float* scale, const float* dx_add,
+                         float* dx, float* dA, float* dB, void* ws, size_t ws_bytes,
+                         moe_stream_t stream) {
+  int st = check_adapters(cfg, n_adapters, rank);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (c.T > 0) {
+    MOE_REQUIRE(x);
+    MOE_REQUIRE(u);
+    MOE_REQUIRE(dy);
+    MOE_REQUIRE(dx);
+  }
+  MOE_REQUIRE(A);
+  MOE_REQUIRE(B);
+  MOE_REQUIRE(scale);
+  MOE_REQUIRE(dA);
+  MOE_REQUIRE(dB);
+  MOE_ALIGNED16(x);
+  MOE_ALIGNED16(u);
+  MOE_ALIGNED16(dy);
+  MOE_ALIGNED16(A);
+  MOE_ALIGNED16(B);
+  MOE_ALIGNED16(dx_add);
+  MOE_ALIGNED16(dx);
+  MOE_ALIGNED16(dA);
+  MOE_ALIGNED16(dB);
+  if ((st = check_sized_ws(plan, plan_bytes, adapter_plan_layout(c, n_adapters).total, "plan")) !=
+      MOE_OK)
+    return st;
+  const AdapterWsLayout W = adapter_ws_layout(c, n_adapters, rank);
+  if ((st = check_sized_ws(ws, ws_bytes, W.total, "workspace")) != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const AdapterCall a{&c, n_adapters, rank, c.d_out, c.d, plan,
+                      static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(B),
+                      static_cast<const __nv_bfloat16*>(A), scale, dx_add, dx,
+                      at<float>(ws, W.v)};
+  cudaError_t e = launch_adapter(a, true, s);
+  if (e == cudaSuccess)
+    e = launch_adapter_grad(c, n_adapters, rank, plan, x, u, dy, dA, dB, ws, s);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_adapter_backward");
 }
 
 int moe_check_wait_timeout(void* ws, size_t ws_bytes, uint32_t limit_us, moe_stream_t stream) {

@@ -20,6 +20,7 @@ enum DeviceError : int32_t {
   kDevBadOffsets = 2,         // offsets not monotone or beyond the row buffer
   kDevBadPerm = 3,            // a gathered row index outside [0, T)
   kDevBadShard = 4,           // this rank's row of all_counts differs from its own counts
+  kDevBadPlan = 5,            // an adapter plan made for other sizes (or not made)
   kDevTimeoutProducer = 16,   // TMA producer gave up waiting for a free stage
   kDevTimeoutMma = 17,        // MMA issuer gave up waiting for data / accumulator
   kDevTimeoutEpilogue = 18,   // epilogue gave up waiting for an accumulator
@@ -455,6 +456,8 @@ __device__ __forceinline__ void pdl_wait_and_release() {
 }
 
 // ------------------------------------------------------------- small utils --
+
+__device__ __forceinline__ int ceil_div_dev(int a, int b) { return (a + b - 1) / b; }
 
 // *p += v at GPU scope with acquire-release order: the calling thread's
 // earlier writes become visible to any thread whose later acquire operation

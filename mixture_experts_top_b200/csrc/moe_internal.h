@@ -264,7 +264,80 @@ cudaError_t launch_route_backward(const moe_config_t& c, const void* x, const fl
                                   const float* f, const float* dgates, const float* daux,
                                   int T_batch, float* dx, float* dW, float* dbias,
                                   float* dlogits, float* dw_part, float* dbias_part,
-                                  cudaStream_t s);
+                                  cudaStream_t s, const float* dlogits_add = nullptr);
+// Workspace of the per-sequence balance loss (balance.cu): control block
+// (error word; the finish launch's counter at byte 64), per-piece partial
+// sums, per-sequence terms.
+struct BalanceLayout {
+  size_t ctrl, p, c, n, z, terms, total;
+};
+BalanceLayout balance_layout(const moe_config_t& c, int n_seqs);
+// off (S+1) or nullptr (S = 1, all tokens); mask (T) or nullptr.
+cudaError_t launch_balance_loss(const moe_config_t& c, int S, const int32_t* off,
+                                const uint8_t* mask, const float* logits, const int32_t* idx,
+                                int32_t* counts, float* prob_mean, int32_t* tokens, float* losses,
+                                void* ws, cudaStream_t s);
+cudaError_t launch_balance_loss_backward(const moe_config_t& c, int S, const int32_t* off,
+                                         const uint8_t* mask, const float* logits,
+                                         const int32_t* counts, const int32_t* tokens,
+                                         const float* dlosses, float* dlogits, void* ws,
+                                         cudaStream_t s);
+
+// The counter-based dropout (dropout.cuh, dropout.cu).
+struct DropArgs {
+  uint32_t thr;                // an element is kept where its 16 bits are >= thr
+  float scale;                 // 65536 / (65536 - thr)
+  uint64_t seed, offset;
+  const uint64_t* offset_dev;  // added to offset, or nullptr
+  uint64_t block0;             // the first row's first block of 8
+};
+cudaError_t launch_dropout(long long rows, int width, bool bf16, const void* x, const void* add,
+                           void* out, const DropArgs& d, cudaStream_t s);
+cudaError_t launch_combine_dropout(const moe_config_t& c, const float* y_perm, const int32_t* dest,
+                                   const float* gates, const void* residual, void* out,
+                                   const DropArgs& d, cudaStream_t s);
+cudaError_t launch_combine_dropout_backward(const moe_config_t& c, const void* dy,
+                                            const float* y_perm, const int32_t* dest,
+                                            const float* gates, float* dy_perm, float* dgates,
+                                            const DropArgs& d, cudaStream_t s);
+
+// Low-rank adapters (adapter.cu).
+constexpr int kAdapterMaxCount = 1024;
+constexpr int kAdapterMaxRank = 128;
+struct AdapterPlanLayout {
+  size_t ctrl;      // error word (256 bytes, the header in them)
+  size_t header;    // int32: T, n, tiles
+  size_t offsets;   // (n + 2) int32: rows of adapter a; group n: no adapter
+  size_t rows;      // (T) int32: tokens by group, in token order
+  size_t tiles;     // int4: group, first row, rows
+  size_t total;
+};
+AdapterPlanLayout adapter_plan_layout(const moe_config_t& c, int n);
+// v (T, r) fp32 and the parts of split adapters' gradients.
+struct AdapterWsLayout {
+  size_t v, part, total;
+};
+AdapterWsLayout adapter_ws_layout(const moe_config_t& c, int n, int r);
+cudaError_t launch_adapter_plan(const moe_config_t& c, int n, const int32_t* ids, void* plan,
+                                cudaStream_t s);
+// Two products of every row tile: forward in = x, K = d, N = d_out, out and
+// base bf16; backward in = dy, K = d_out, N = d, out and base fp32, W1 = B,
+// W2 = A, u = v.
+struct AdapterCall {
+  const moe_config_t* c;
+  int n, r, K, N;
+  void* plan;
+  const __nv_bfloat16 *in, *W1, *W2;
+  const float* scale;
+  const void* base;
+  void* out;
+  float* u;
+};
+cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s);
+cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan, const void* x,
+                                const float* u, const void* dy, float* dA, float* dB, void* ws,
+                                cudaStream_t s);
+
 // One bounded mbarrier wait that nothing completes; after limit_ns the kernel
 // writes the self-test code to err and returns (moe_api.cu).
 cudaError_t launch_wait_self_test(int32_t* err, uint64_t limit_ns, cudaStream_t s);
