@@ -1,4 +1,5 @@
-"""Python binding of ``libmoe_b200.so`` (the C ABI in ``include/moe.h``).
+"""Python binding of ``libmoe_b200.so`` (the C ABI in ``include/moe.h`` and
+``include/moe_packed.h``).
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels.  torch tensors supply device pointers and torch supplies the current
@@ -23,7 +24,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUD
 EXPERT_KINDS = {"linear": 0, "relu": 1, "swiglu": 2}
 DTYPES = {"f32": 0, "bf16": 1}
 
-# Every symbol the header declares, with its ctypes signature.
+# Every symbol include/moe.h declares, with its ctypes signature.
 _c_p = ctypes.c_void_p
 _SIGNATURES = {
     "moe_workspace_size": (ctypes.c_size_t, [_c_p]),
@@ -57,6 +58,12 @@ _SIGNATURES = {
     "moe_expert_ffn_combine": (ctypes.c_int, [_c_p] * 11 + [ctypes.c_size_t, _c_p]),
     "moe_forward_combine_fused": (ctypes.c_int, [_c_p, _c_p]),
     "moe_forward": (ctypes.c_int, [_c_p] * 15 + [ctypes.c_size_t, _c_p]),
+    "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
+    "moe_last_error_message": (ctypes.c_char_p, []),
+}
+
+# Every symbol include/moe_packed.h declares.
+_PACKED_SIGNATURES = {
     "moe_balance_workspace_size": (ctypes.c_size_t, [_c_p, ctypes.c_int32]),
     "moe_balance_loss": (ctypes.c_int, [_c_p, ctypes.c_int32] + [_c_p] * 9
                          + [ctypes.c_size_t, _c_p]),
@@ -74,8 +81,6 @@ _SIGNATURES = {
     "moe_adapter_workspace_size": (ctypes.c_size_t, [_c_p] + [ctypes.c_int32] * 2),
     "moe_adapter_backward": (ctypes.c_int, [_c_p] + [ctypes.c_int32] * 2
                              + [_c_p, ctypes.c_size_t] + [_c_p] * 11 + [ctypes.c_size_t, _c_p]),
-    "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
-    "moe_last_error_message": (ctypes.c_char_p, []),
 }
 
 
@@ -129,7 +134,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_NAME} not found at {path}: build it with "
                                "`python -m mixture_experts_top_b200.build` (needs nvcc)")
         lib = ctypes.CDLL(path)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **_PACKED_SIGNATURES}.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -138,7 +143,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def exported_symbols() -> list:
+    """The entry points of include/moe.h."""
     return list(_SIGNATURES)
+
+
+def packed_symbols() -> list:
+    """The entry points of include/moe_packed.h."""
+    return list(_PACKED_SIGNATURES)
 
 
 def _ptr(t) -> Optional[int]:
@@ -153,8 +164,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the handle alone: a Stream object costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -378,33 +389,30 @@ def moe_forward(cfg, x, W_router, logit_bias, noise, W_in, W_up, W_out, output, 
 # These calls take many tensors of related shapes, so the binding checks each
 # one's type, shape and device before the library sees its pointer.
 
-def _arg(t, name: str, dtype, shape) -> Optional[int]:
-    """Pointer of a contiguous tensor of this type and shape on the current
-    device (shape None: any)."""
+def _arg(t, name: str, dtype, shape, dev: int) -> Optional[int]:
+    """Pointer of a contiguous tensor of this type and shape (None: any) on
+    CUDA device `dev`, the current one."""
+    if (t.dtype is dtype and (shape is None or t.shape == shape) and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != _current_device():
+    if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be on the current CUDA device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name: str, dtype, shape) -> Optional[int]:
-    return None if t is None else _arg(t, name, dtype, shape)
+def _opt(t, name: str, dtype, shape, dev: int) -> Optional[int]:
+    return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
-def _current_device() -> int:
+def _device() -> int:
+    """The current device, which the call's tensors must be on (-2, no
+    tensor's device, before CUDA is initialised)."""
     import torch
-    return torch.cuda.current_device()
-
-
-def _buffer(t, name: str):
-    """Pointer and bytes of a workspace or plan (uint8)."""
-    import torch
-    return _arg(t, name, torch.uint8, None), t.numel()
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
 def _act(cfg):
@@ -412,14 +420,13 @@ def _act(cfg):
     return torch.bfloat16 if cfg.act_dtype == DTYPES["bf16"] else torch.float32
 
 
-def _seqs(seq_offsets):
+def _seqs(seq_offsets, i32, dev):
     """Number of sequences and the offsets' pointer (None: one sequence)."""
-    import torch
     if seq_offsets is None:
         return 1, None
     if seq_offsets.dim() != 1:
         raise ValueError("seq_offsets must have one dimension")
-    return seq_offsets.numel() - 1, _arg(seq_offsets, "seq_offsets", torch.int32, None)
+    return seq_offsets.numel() - 1, _arg(seq_offsets, "seq_offsets", i32, None, dev)
 
 
 def _sized(n: int, where: str) -> int:
@@ -449,18 +456,19 @@ def alloc_balance_workspace(cfg: MoeConfig, n_seqs: int, device="cuda", stream=N
 def moe_balance_loss(cfg, seq_offsets, token_mask, logits, expert_indices, counts, prob_mean,
                      tokens, losses, ws, stream=None) -> None:
     """seq_offsets (n_seqs+1) int32 or None (one sequence: all tokens);
-    token_mask (T) uint8 or None; see include/moe.h for the outputs."""
+    token_mask (T) uint8 or None; see include/moe_packed.h for the outputs."""
     import torch
     f32, i32 = torch.float32, torch.int32
-    n, off = _seqs(seq_offsets)
+    dev = _device()
+    n, off = _seqs(seq_offsets, i32, dev)
     T, E = cfg.T, cfg.E
-    wp, wn = _buffer(ws, "ws")
+    wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
     _check(load_library().moe_balance_loss(
-        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,)),
-        _arg(logits, "logits", f32, (T, E)),
-        _arg(expert_indices, "expert_indices", i32, (T, cfg.top_k)),
-        _arg(counts, "counts", i32, (n, E)), _arg(prob_mean, "prob_mean", f32, (n, E)),
-        _arg(tokens, "tokens", i32, (n + 2,)), _arg(losses, "losses", f32, (2,)), wp, wn,
+        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,), dev),
+        _arg(logits, "logits", f32, (T, E), dev),
+        _arg(expert_indices, "expert_indices", i32, (T, cfg.top_k), dev),
+        _arg(counts, "counts", i32, (n, E), dev), _arg(prob_mean, "prob_mean", f32, (n, E), dev),
+        _arg(tokens, "tokens", i32, (n + 2,), dev), _arg(losses, "losses", f32, (2,), dev), wp, wn,
         _stream(stream)), "moe_balance_loss")
 
 
@@ -468,14 +476,15 @@ def moe_balance_loss_backward(cfg, seq_offsets, token_mask, logits, counts, toke
                               dlogits, ws, stream=None) -> None:
     import torch
     f32, i32 = torch.float32, torch.int32
-    n, off = _seqs(seq_offsets)
+    dev = _device()
+    n, off = _seqs(seq_offsets, i32, dev)
     T, E = cfg.T, cfg.E
-    wp, wn = _buffer(ws, "ws")
+    wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
     _check(load_library().moe_balance_loss_backward(
-        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,)),
-        _arg(logits, "logits", f32, (T, E)), _arg(counts, "counts", i32, (n, E)),
-        _arg(tokens, "tokens", i32, (n + 2,)), _arg(dlosses, "dlosses", f32, (2,)),
-        _arg(dlogits, "dlogits", f32, (T, E)), wp, wn, _stream(stream)),
+        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,), dev),
+        _arg(logits, "logits", f32, (T, E), dev), _arg(counts, "counts", i32, (n, E), dev),
+        _arg(tokens, "tokens", i32, (n + 2,), dev), _arg(dlosses, "dlosses", f32, (2,), dev),
+        _arg(dlogits, "dlogits", f32, (T, E), dev), wp, wn, _stream(stream)),
         "moe_balance_loss_backward")
 
 
@@ -484,7 +493,8 @@ def moe_route_backward_add(cfg, x, W_router, logits, expert_indices, gates, f, d
                            stream=None) -> None:
     """moe_route_backward with dlogits_add (T, E) fp32 added to the logits' gradient."""
     import torch
-    add = _arg(dlogits_add, "dlogits_add", torch.float32, (cfg.T, cfg.E))
+    dev = _device()
+    add = _arg(dlogits_add, "dlogits_add", torch.float32, (cfg.T, cfg.E), dev)
     _check(load_library().moe_route_backward_add(
         ctypes.byref(cfg), _ptr(x), _ptr(W_router), _ptr(logits), _ptr(expert_indices),
         _ptr(gates), _ptr(f), _ptr(dgates), _ptr(daux), int(T_batch), add, _ptr(dx),
@@ -492,13 +502,13 @@ def moe_route_backward_add(cfg, x, W_router, logits, expert_indices, gates, f, d
         "moe_route_backward_add")
 
 
-def _drop(p, seed, offset, token_base):
+def _drop(p, seed, offset, token_base, dev):
     """moe_dropout_t; offset is an int, or a one-element int64 CUDA tensor that
     the kernel reads when it runs (fresh masks from one captured graph)."""
     if isinstance(offset, int):
         return MoeDropout(p, seed, offset, None, token_base)
     import torch
-    return MoeDropout(p, seed, 0, _arg(offset, "offset", torch.int64, (1,)), token_base)
+    return MoeDropout(p, seed, 0, _arg(offset, "offset", torch.int64, (1,), dev), token_base)
 
 
 def moe_dropout(cfg, p, seed, offset, token_base, x, add, out, stream=None) -> None:
@@ -510,23 +520,26 @@ def moe_dropout(cfg, p, seed, offset, token_base, x, add, out, stream=None) -> N
         raise ValueError(f"x must be bfloat16 or float32, got {dt}")
     if len(shape) != 2 or shape[0] != cfg.T:
         raise ValueError(f"x must have shape ({cfg.T}, width), got {tuple(shape)}")
-    d = _drop(p, seed, offset, token_base)
+    dev = _device()
+    d = _drop(p, seed, offset, token_base, dev)
     _check(load_library().moe_dropout(
         ctypes.byref(cfg), ctypes.byref(d), shape[1],
-        DTYPES["bf16"] if dt is torch.bfloat16 else DTYPES["f32"], _arg(x, "x", dt, None),
-        _opt(add, "add", dt, shape), _arg(out, "out", dt, shape), _stream(stream)), "moe_dropout")
+        DTYPES["bf16"] if dt is torch.bfloat16 else DTYPES["f32"], _arg(x, "x", dt, None, dev),
+        _opt(add, "add", dt, shape, dev), _arg(out, "out", dt, shape, dev), _stream(stream)),
+        "moe_dropout")
 
 
 def moe_combine_dropout(cfg, p, seed, offset, token_base, y_perm, dest, gates, residual, output,
                         stream=None) -> None:
     """moe_combine with dropout, plus residual (or None) added after it."""
     import torch
-    act, T, k, w = _act(cfg), cfg.T, cfg.top_k, cfg.d_out
-    d = _drop(p, seed, offset, token_base)
+    f32, act, T, k, w = torch.float32, _act(cfg), cfg.T, cfg.top_k, cfg.d_out
+    dev = _device()
+    d = _drop(p, seed, offset, token_base, dev)
     _check(load_library().moe_combine_dropout(
-        ctypes.byref(cfg), ctypes.byref(d), _arg(y_perm, "y_perm", torch.float32, (T * k, w)),
-        _arg(dest, "dest", torch.int32, (T, k)), _arg(gates, "gates", torch.float32, (T, k)),
-        _opt(residual, "residual", act, (T, w)), _arg(output, "output", act, (T, w)),
+        ctypes.byref(cfg), ctypes.byref(d), _arg(y_perm, "y_perm", f32, (T * k, w), dev),
+        _arg(dest, "dest", torch.int32, (T, k), dev), _arg(gates, "gates", f32, (T, k), dev),
+        _opt(residual, "residual", act, (T, w), dev), _arg(output, "output", act, (T, w), dev),
         _stream(stream)), "moe_combine_dropout")
 
 
@@ -534,12 +547,13 @@ def moe_combine_dropout_backward(cfg, p, seed, offset, token_base, dy, y_perm, d
                                  dy_perm, dgates, stream=None) -> None:
     import torch
     f32, act, T, k, w = torch.float32, _act(cfg), cfg.T, cfg.top_k, cfg.d_out
-    d = _drop(p, seed, offset, token_base)
+    dev = _device()
+    d = _drop(p, seed, offset, token_base, dev)
     _check(load_library().moe_combine_dropout_backward(
-        ctypes.byref(cfg), ctypes.byref(d), _arg(dy, "dy", act, (T, w)),
-        _arg(y_perm, "y_perm", f32, (T * k, w)), _arg(dest, "dest", torch.int32, (T, k)),
-        _arg(gates, "gates", f32, (T, k)), _arg(dy_perm, "dy_perm", f32, (T * k, w)),
-        _arg(dgates, "dgates", f32, (T, k)), _stream(stream)), "moe_combine_dropout_backward")
+        ctypes.byref(cfg), ctypes.byref(d), _arg(dy, "dy", act, (T, w), dev),
+        _arg(y_perm, "y_perm", f32, (T * k, w), dev), _arg(dest, "dest", torch.int32, (T, k), dev),
+        _arg(gates, "gates", f32, (T, k), dev), _arg(dy_perm, "dy_perm", f32, (T * k, w), dev),
+        _arg(dgates, "dgates", f32, (T, k), dev), _stream(stream)), "moe_combine_dropout_backward")
 
 
 def moe_adapter_plan_size(cfg: MoeConfig, n_adapters: int) -> int:
@@ -568,10 +582,11 @@ def alloc_adapter_workspace(cfg: MoeConfig, n_adapters: int, rank: int, device="
 def moe_adapter_plan(cfg, n_adapters, token_adapter, plan, stream=None) -> None:
     """Groups the tokens by adapter: token_adapter (T) int32, negative for none."""
     import torch
-    pp, pn = _buffer(plan, "plan")
+    dev = _device()
+    pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
     _check(load_library().moe_adapter_plan(
         ctypes.byref(cfg), int(n_adapters),
-        _arg(token_adapter, "token_adapter", torch.int32, (cfg.T,)), pp, pn, _stream(stream)),
+        _arg(token_adapter, "token_adapter", torch.int32, (cfg.T,), dev), pp, pn, _stream(stream)),
         "moe_adapter_plan")
 
 
@@ -586,12 +601,14 @@ def moe_adapter(cfg, plan, x, A, B, scale, base, output, u, stream=None) -> None
     import torch
     bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
     n, r = _adapter_shape(cfg, A)
-    pp, pn = _buffer(plan, "plan")
+    dev = _device()
+    pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
     _check(load_library().moe_adapter(
-        ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d)), _arg(A, "A", bf, None),
-        _arg(B, "B", bf, (n, r, w)), _arg(scale, "scale", f32, (n,)),
-        _opt(base, "base", bf, (T, w)), _arg(output, "output", bf, (T, w)),
-        _opt(u, "u", f32, (T, r)), _stream(stream)), "moe_adapter")
+        ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d), dev),
+        _arg(A, "A", bf, None, dev),
+        _arg(B, "B", bf, (n, r, w), dev), _arg(scale, "scale", f32, (n,), dev),
+        _opt(base, "base", bf, (T, w), dev), _arg(output, "output", bf, (T, w), dev),
+        _opt(u, "u", f32, (T, r), dev), _stream(stream)), "moe_adapter")
 
 
 def moe_adapter_backward(cfg, plan, x, u, dy, A, B, scale, dx_add, dx, dA, dB, ws,
@@ -599,11 +616,14 @@ def moe_adapter_backward(cfg, plan, x, u, dy, A, B, scale, dx_add, dx, dA, dB, w
     import torch
     bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
     n, r = _adapter_shape(cfg, A)
-    pp, pn = _buffer(plan, "plan")
-    wp, wn = _buffer(ws, "ws")
+    dev = _device()
+    pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
+    wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
     _check(load_library().moe_adapter_backward(
-        ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d)), _arg(u, "u", f32, (T, r)),
-        _arg(dy, "dy", bf, (T, w)), _arg(A, "A", bf, None), _arg(B, "B", bf, (n, r, w)),
-        _arg(scale, "scale", f32, (n,)), _opt(dx_add, "dx_add", f32, (T, cfg.d)),
-        _arg(dx, "dx", f32, (T, cfg.d)), _arg(dA, "dA", f32, A.shape),
-        _arg(dB, "dB", f32, (n, r, w)), wp, wn, _stream(stream)), "moe_adapter_backward")
+        ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d), dev),
+        _arg(u, "u", f32, (T, r), dev),
+        _arg(dy, "dy", bf, (T, w), dev), _arg(A, "A", bf, None, dev),
+        _arg(B, "B", bf, (n, r, w), dev),
+        _arg(scale, "scale", f32, (n,), dev), _opt(dx_add, "dx_add", f32, (T, cfg.d), dev),
+        _arg(dx, "dx", f32, (T, cfg.d), dev), _arg(dA, "dA", f32, A.shape, dev),
+        _arg(dB, "dB", f32, (n, r, w), dev), wp, wn, _stream(stream)), "moe_adapter_backward")

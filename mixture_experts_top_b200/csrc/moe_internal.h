@@ -10,7 +10,7 @@
 #include <utility>
 #include <stdint.h>
 
-#include "../../include/moe.h"
+#include "../../include/moe_packed.h"
 
 namespace moe {
 

@@ -2,6 +2,8 @@
 host, before any CUDA call, so this file needs no GPU.  Pointers are host
 addresses that are never followed."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -23,6 +25,16 @@ def _drop(p=0.1, token_base=0, offset_dev=None):
 
 def _call(lib, name, cfg, *args):
     return getattr(lib, name)(ctypes.byref(cfg) if cfg is not None else None, *args)
+
+
+def test_every_declared_symbol_is_exported(moe_lib):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "moe_packed.h")).read(),
+                  flags=re.S)
+    names = sorted(set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text)))
+    assert names == sorted(api.packed_symbols()) and len(names) == 12
+    for n in names:
+        assert hasattr(moe_lib, n), n
 
 
 def test_balance_refusals(moe_lib):
