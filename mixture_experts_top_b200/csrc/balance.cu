@@ -15,9 +15,9 @@
 //
 // Both directions are one pass over the logits: bound by HBM for large T x E,
 // by launch latency below about a million logits.  A token's E logits sit in
-// the registers of G = min(32, E rounded up to a power of 2) lanes, so a warp
-// works on 32 / G tokens at once; maximum and sum are butterflies over the G
-// lanes, in fp32.
+// the registers of G <= 16 lanes (32 where they cannot be read by 16-byte
+// vectors), so a warp works on 32 / G tokens at once; maximum and sum are
+// butterflies over the G lanes, in fp32.
 //
 // Summation order (no floating-point atomics, nothing depends on which CTA
 // runs first): a warp owns C consecutive tokens and walks the sequences that
@@ -27,15 +27,13 @@
 // one sequence covers all 8 warps of a CTA, their sums are added in warp
 // order and only the first warp's slot is written.  The second launch adds a
 // sequence's slots in a fixed order in fp64.
-#include <type_traits>
-
 #include "moe_device.cuh"
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kLogWarps = 3, kWarps = 1 << kLogWarps;
 
 // The number of i in [1, S] with off[i] <= t, for non-decreasing off: the
 // sequence that holds token t if off[0] <= t < off[S].  32 samples a round.
@@ -55,16 +53,19 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* __restrict__ off, in
   return lo;
 }
 
-// Bounds of sequence s inside [0, T] whatever the offsets hold.
-__device__ __forceinline__ void seq_bounds(const int32_t* __restrict__ off, int s, int T, int& lo,
+// Bounds of sequence s inside [0, T] whatever the offsets hold; false if they
+// had to be moved there.
+__device__ __forceinline__ bool seq_bounds(const int32_t* __restrict__ off, int s, int T, int& lo,
                                            int& hi) {
   if (off == nullptr) {
     lo = 0;
     hi = T;
-    return;
+    return true;
   }
-  lo = min(max(__ldg(off + s), 0), T);
-  hi = min(max(__ldg(off + s + 1), lo), T);
+  const int a = __ldg(off + s), b = __ldg(off + s + 1);
+  lo = min(max(a, 0), T);
+  hi = min(max(b, lo), T);
+  return lo == a && hi == b;
 }
 
 template <int G>
@@ -80,34 +81,88 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// This lane's logits of token t: experts gl + G q.  Tokens not counted are
-// not read (they may hold anything).
-template <int G, int Q>
-__device__ __forceinline__ void load_logits(const float* __restrict__ logits, int t, bool act,
-                                            int E, int gl, float (&L)[Q]) {
+// How a token's experts lie in the G lanes of its group: NV a lane, by 16-byte
+// vectors (VEC: E a multiple of 4, rows 16-byte aligned) or one by one.
+template <int G_, int NV_, bool VEC_>
+struct Lanes {
+  static constexpr int G = G_, NV = NV_;
+  static constexpr bool VEC = VEC_;
+  static constexpr int W = 32 / G;   // tokens a warp works on at once
+  // The expert of this lane's value i.
+  static __device__ __forceinline__ int expert(int gl, int i) {
+    return VEC ? 4 * (gl + G * (i / 4)) + i % 4 : gl + G * i;
+  }
+};
+
+// This lane's logits of token t; -inf where there is none.
+template <typename L>
+__device__ __forceinline__ void load_logits(const float* __restrict__ logits, int t, bool in,
+                                            int E, int gl, float (&v)[L::NV]) {
   const float* row = logits + (size_t)t * E;
+  if constexpr (L::VEC) {
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const int e = gl + G * q;
-    L[q] = act && e < E ? __ldg(row + e) : -INFINITY;
+    for (int i = 0; i < L::NV; i += 4) {
+      const int e = L::expert(gl, i);
+      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (in && e < E) q = __ldg(reinterpret_cast<const float4*>(row + e));
+      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < L::NV; ++i) {
+      const int e = L::expert(gl, i);
+      v[i] = in && e < E ? __ldg(row + e) : -INFINITY;
+    }
   }
 }
 
-// exp(l - max) of this lane's experts, their sum's inverse and the token's
-// log-sum-exp, from the G lanes' logits; all 0 where act is false.
-template <int G, int Q>
-__device__ __forceinline__ void softmax_terms(float (&L)[Q], bool act, float& inv, float& lse) {
-  float m = L[0];
+// This lane's values of a row of E floats to memory.
+template <typename L>
+__device__ __forceinline__ void store_values(float* row, int E, int gl, const float (&v)[L::NV]) {
+  if constexpr (L::VEC) {
 #pragma unroll
-  for (int q = 1; q < Q; ++q) m = fmaxf(m, L[q]);
-  m = group_max<G>(m);
+    for (int i = 0; i < L::NV; i += 4) {
+      const int e = L::expert(gl, i);
+      if (e < E)
+        *reinterpret_cast<float4*>(row + e) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < L::NV; ++i) {
+      const int e = L::expert(gl, i);
+      if (e < E) row[e] = v[i];
+    }
+  }
+}
+
+// exp(d) for d <= 0 as 2^(d log2 e): one product and the hardware's 2^x, within
+// 2.3 |d| + 4 half steps of fp32.  With expf, whose exact range reduction is six
+// more instructions a logit, instructions and not HBM bound these kernels: the
+// forward's first launch took 57 us, against 44, at 131072 x 256.
+__device__ __forceinline__ float exp_neg(float d) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.44269504f));
+  return r;
+}
+
+// exp(l - max) of this lane's experts, their sum's inverse and the token's
+// log-sum-exp, from the G lanes' logits; all 0 where act is false (the logits
+// may then hold anything).
+template <typename L>
+__device__ __forceinline__ void softmax_terms(float (&v)[L::NV], bool act, float& inv,
+                                              float& lse) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < L::NV; ++i) m = fmaxf(m, v[i]);
+  m = group_max<L::G>(m);
   float sum = 0.f;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    L[q] = act ? expf(L[q] - m) : 0.f;
-    sum += L[q];
+  for (int i = 0; i < L::NV; ++i) {
+    const float ex = exp_neg(v[i] - m);
+    v[i] = act ? ex : 0.f;
+    sum += v[i];
   }
-  sum = group_sum<G>(sum);
+  sum = group_sum<L::G>(sum);
   inv = act ? 1.f / sum : 0.f;
   lse = act ? m + logf(sum) : 0.f;
 }
@@ -119,63 +174,270 @@ struct BalanceParts {
   float* z;        // (slots) sums of lse^2
 };
 
-template <int G, int Q>
-__global__ void __launch_bounds__(256)
+// The slots of a sequence [lo, hi) in order: the warps of a CTA it covers in
+// part, one per CTA it covers whole, the warps of the last CTA in part.
+struct SeqSlots {
+  int s, first, nh, jm, nm, tail, nt;
+  __device__ SeqSlots(int s_, int lo, int hi, int T, int lc) : s(s_) {
+    first = nh = jm = nm = tail = nt = 0;
+    if (lo >= hi) return;
+    const int lcc = lc + kLogWarps;   // log2 of a CTA's tokens
+    const int j0 = lo >> lcc, j1 = (hi - 1) >> lcc;
+    const bool from = lo == j0 << lcc;
+    const bool upto = hi >= (int)min((long long)T, (long long)(j1 + 1) << lcc);
+    first = lo >> lc;
+    if (j0 == j1 && !(from && upto)) {
+      nh = ((hi - 1) >> lc) - first + 1;
+      return;
+    }
+    jm = from ? j0 : j0 + 1;
+    nh = from ? 0 : (j0 + 1) * kWarps - first;
+    nm = (upto ? j1 + 1 : j1) - jm;
+    tail = j1 * kWarps;
+    nt = upto ? 0 : ((hi - 1) >> lc) - tail + 1;
+  }
+  __device__ int count() const { return nh + nm + nt; }
+  __device__ size_t operator()(int i) const {
+    const int w = i < nh ? first + i : i < nh + nm ? kWarps * (jm + i - nh) : tail + (i - nh - nm);
+    return (size_t)w + s;
+  }
+};
+
+struct BalanceOut {
+  int32_t* counts;     // (S, E)
+  float* prob_mean;    // (S, E)
+  int32_t* tokens;     // (S + 2)
+  float* losses;       // (2)
+  double* terms;       // (S, 2): a sequence's share of both losses
+};
+
+// A CTA's shared memory for the sums below; EP threads (a power of two >= E)
+// stand for the experts, NT / EP groups of them walk a sequence's slots.
+template <int NT>
+struct FinishSmem {
+  double p[NT];
+  int32_t c[NT];
+  double d[2][NT / 32];
+  int32_t i[2][NT / 32];
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Counts, P, n and the loss terms of sequence s, by the whole CTA.
+template <int NT>
+__device__ void finish_sequence(FinishSmem<NT>& sm, const BalanceParts& part,
+                                const int32_t* __restrict__ off, int s, int T, int E, int k, int lc,
+                                int EP, const BalanceOut& out, int32_t* err) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ng = NT / EP, e = tid & (EP - 1), gi = tid / EP;
+  int lo, hi;
+  if (!seq_bounds(off, s, T, lo, hi) && tid == 0) report_error(err, kDevBadOffsets);
+  const SeqSlots slots(s, lo, hi, T, lc);
+  const int ni = slots.count();
+  double p = 0.0, z = 0.0;
+  int c = 0, n = 0;
+  for (int i = tid; i < ni; i += NT) {
+    const size_t at = slots(i);
+    n += __ldcg(part.n + at);
+    z += (double)__ldcg(part.z + at);
+  }
+  if (e < E) {
+    constexpr int U = 8;   // slots in flight
+    for (int i = gi; i < ni; i += U * ng) {
+      float pv[U];
+      int cv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = i + u * ng < ni;
+        const size_t at = in ? slots(i + u * ng) * E + e : 0;
+        pv[u] = in ? __ldcg(part.p + at) : 0.f;
+        cv[u] = in ? __ldcg(part.c + at) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        p += (double)pv[u];
+        c += cv[u];
+      }
+    }
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  z = warp_sum(z);
+  __syncthreads();   // the last sequence's sums have been read
+  sm.p[tid] = p;
+  sm.c[tid] = c;
+  if (lane == 0) {
+    sm.i[0][warp] = n;
+    sm.d[0][warp] = z;
+  }
+  __syncthreads();
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) n += sm.i[0][w];
+  double term = 0.0;
+  if (tid < E) {
+    p = 0.0;
+    c = 0;
+    for (int j = 0; j < ng; ++j) {
+      p += sm.p[j * EP + tid];
+      c += sm.c[j * EP + tid];
+    }
+    const double inv = n > 0 ? 1.0 / (double)n : 0.0;
+    const double P = p * inv;
+    out.counts[(size_t)s * E + tid] = c;
+    out.prob_mean[(size_t)s * E + tid] = (float)P;
+    term = (double)c * inv * P;   // k f P
+  }
+  term = warp_sum(term);
+  if (lane == 0) sm.d[1][warp] = term;
+  __syncthreads();
+  if (tid == 0) {
+    z = term = 0.0;
+    for (int w = 0; w < NT / 32; ++w) {
+      z += sm.d[0][w];
+      term += sm.d[1][w];
+    }
+    out.tokens[s] = n;
+    out.terms[2 * (size_t)s] = term * E / k;
+    out.terms[2 * (size_t)s + 1] = z;
+  }
+}
+
+// The sequences' terms into the losses, N and S+, by the whole CTA.
+template <int NT>
+__device__ void finish_totals(FinishSmem<NT>& sm, int S, const BalanceOut& out) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  double b = 0.0, z = 0.0;
+  int n = 0, live = 0;
+  for (int s = tid; s < S; s += NT) {
+    const int ns = __ldcg(out.tokens + s);
+    b += __ldcg(out.terms + 2 * (size_t)s);
+    z += __ldcg(out.terms + 2 * (size_t)s + 1);
+    n += ns;
+    live += ns > 0;
+  }
+  b = warp_sum(b);
+  z = warp_sum(z);
+  n = __reduce_add_sync(0xffffffffu, n);
+  live = __reduce_add_sync(0xffffffffu, live);
+  __syncthreads();
+  if (lane == 0) {
+    sm.d[0][warp] = b;
+    sm.d[1][warp] = z;
+    sm.i[0][warp] = n;
+    sm.i[1][warp] = live;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    b = z = 0.0;
+    n = live = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+      b += sm.d[0][w];
+      z += sm.d[1][w];
+      n += sm.i[0][w];
+      live += sm.i[1][w];
+    }
+    out.losses[0] = live > 0 ? (float)(b / (double)live) : 0.f;
+    out.losses[1] = n > 0 ? (float)(z / (double)n) : 0.f;
+    out.tokens[S] = n;
+    out.tokens[S + 1] = live;
+  }
+}
+
+// True in every thread of the last CTA of the grid to get here; what the
+// others wrote before is then visible through L2.
+__device__ __forceinline__ bool last_cta(unsigned* done) {
+  __shared__ bool last;
+  __syncthreads();   // the release below covers the whole CTA's writes
+  if (threadIdx.x == 0) {
+    last = atom_add_acq_rel_gpu(done, 1u) == gridDim.x - 1;
+    if (last) *done = 0;
+  }
+  __syncthreads();
+  return last;
+}
+
+// FUSED: the last CTA also adds up the sequences (few CTAs and sequences:
+// the second launch would cost more than its work).
+template <typename L, bool FUSED>
+__global__ void __launch_bounds__(256, 4)
     balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                            const int32_t* __restrict__ off, const uint8_t* __restrict__ mask,
-                           int T, int E, int k, int S, int C, BalanceParts part, int32_t* err) {
+                           int T, int E, int k, int S, int lc, BalanceParts part, int EP,
+                           BalanceOut out, unsigned* done, int32_t* err) {
   pdl_wait_and_release();
   __shared__ int32_t hist[kWarps][256];
-  __shared__ float red[kWarps][256];
+  __shared__ __align__(16) float red[kWarps][256];
   __shared__ int32_t red_n[kWarps];
   __shared__ float red_z[kWarps];
-  constexpr int W = 32 / G;   // tokens at once
+  __shared__ int first_seq[kWarps];
+  constexpr int G = L::G, W = L::W, NV = L::NV;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane / G, gl = lane % G;
-  const int gw = blockIdx.x * kWarps + warp;
+  const int C = 1 << lc, gw = blockIdx.x * kWarps + warp;
   const int c0 = blockIdx.x * kWarps * C;
   const int c1 = (int)min((long long)T, (long long)c0 + kWarps * C);
   const int t0 = (int)min((long long)c1, (long long)c0 + warp * C);
   const int t1 = (int)min((long long)c1, (long long)t0 + C);
+  // the first tokens' logits are on their way while their sequence is found
+  float nxt[NV];
+  load_logits<L>(logits, t0 + g, t0 + g < t1, E, gl, nxt);
   int lo, hi;
-  const int s0 = off == nullptr ? 0 : warp_find_seq(off, S, c0);
-  bool merged = false;
+  int s = off == nullptr ? 0 : warp_find_seq(off, S, t0);
+  if (lane == 0) first_seq[warp] = s;
+  __syncthreads();
+  const int s0 = first_seq[0];
+  bool merged = false;   // one sequence holds the whole CTA's tokens
   if (s0 < S) {
     seq_bounds(off, s0, T, lo, hi);
     merged = lo <= c0 && hi >= c1;
   }
+  if (merged) s = s0;    // (a warp without tokens may have found another)
   // the rest of the loop runs per warp; merged is the same for all of them
-  for (int s = merged || off == nullptr ? s0 : warp_find_seq(off, S, t0); s < S; ++s) {
+  for (; s < S; ++s) {
     seq_bounds(off, s, T, lo, hi);
     if (!merged && lo >= t1) break;
     const int b = max(lo, t0), e1 = min(hi, t1);
     if (!merged && b >= e1) continue;
+    if (b != t0) load_logits<L>(logits, b + g, b + g < e1, E, gl, nxt);
+    bool nact = b + g < e1 && (mask == nullptr || __ldg(mask + b + g) != 0);
     for (int e = lane; e < E; e += 32) hist[warp][e] = 0;
     __syncwarp();
-    for (int i = b * k + lane; i < e1 * k; i += 32) {
-      if (mask != nullptr && mask[i / k] == 0) continue;
-      const int e = __ldg(idx + i);
-      if ((unsigned)e < (unsigned)E) atomicAdd(&hist[warp][e], 1);
-      else report_error(err, kDevBadExpertIndex);
+    for (int i0 = b * k + lane; i0 < e1 * k; i0 += 128) {
+      int ev[4];
+      bool in[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + 32 * u;
+        in[u] = i < e1 * k;
+        ev[u] = in[u] ? __ldg(idx + i) : 0;
+        if (mask != nullptr && in[u]) in[u] = __ldg(mask + i / k) != 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (!in[u]) continue;
+        if ((unsigned)ev[u] < (unsigned)E) atomicAdd(&hist[warp][ev[u]], 1);
+        else report_error(err, kDevBadExpertIndex);
+      }
     }
-    float acc[Q], z = 0.f;
+    float acc[NV], z = 0.f;
     int n = 0;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) acc[q] = 0.f;
-    float nxt[Q];
-    bool nact = b + g < e1 && (mask == nullptr || mask[b + g] != 0);
-    load_logits<G, Q>(logits, b + g, nact, E, gl, nxt);
+    for (int i = 0; i < NV; ++i) acc[i] = 0.f;
     for (int tb = b; tb < e1; tb += W) {
-      float L[Q], inv, lse;
+      float v[NV], inv, lse;
 #pragma unroll
-      for (int q = 0; q < Q; ++q) L[q] = nxt[q];
+      for (int i = 0; i < NV; ++i) v[i] = nxt[i];
       const bool act = nact;
       const int tn = tb + W + g;
-      nact = tn < e1 && (mask == nullptr || mask[tn] != 0);
-      load_logits<G, Q>(logits, tn, nact, E, gl, nxt);
-      softmax_terms<G, Q>(L, act, inv, lse);
+      nact = tn < e1 && (mask == nullptr || __ldg(mask + tn) != 0);
+      load_logits<L>(logits, tn, tn < e1, E, gl, nxt);
+      softmax_terms<L>(v, act, inv, lse);
 #pragma unroll
-      for (int q = 0; q < Q; ++q) acc[q] = fmaf(L[q], inv, acc[q]);
+      for (int i = 0; i < NV; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
       if (gl == 0 && act) {
         z = fmaf(lse, lse, z);
         ++n;
@@ -184,18 +446,14 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int o = 16; o >= G; o >>= 1) {
 #pragma unroll
-      for (int q = 0; q < Q; ++q) acc[q] += __shfl_xor_sync(0xffffffffu, acc[q], o);
+      for (int i = 0; i < NV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
       z += __shfl_xor_sync(0xffffffffu, z, o);
       n += __shfl_xor_sync(0xffffffffu, n, o);
     }
     __syncwarp();
     if (!merged) {
       const size_t slot = (size_t)gw + s;
-      if (g == 0) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          if (gl + G * q < E) part.p[slot * E + gl + G * q] = acc[q];
-      }
+      if (g == 0) store_values<L>(part.p + slot * E, E, gl, acc);
       for (int e = lane; e < E; e += 32) part.c[slot * E + e] = hist[warp][e];
       if (lane == 0) {
         part.n[slot] = n;
@@ -204,10 +462,7 @@ __global__ void __launch_bounds__(256)
       __syncwarp();
       continue;
     }
-    if (g == 0) {
-#pragma unroll
-      for (int q = 0; q < Q; ++q) red[warp][gl + G * q] = acc[q];
-    }
+    if (g == 0) store_values<L>(red[warp], E, gl, acc);
     if (lane == 0) {
       red_n[warp] = n;
       red_z[warp] = z;
@@ -238,166 +493,46 @@ __global__ void __launch_bounds__(256)
     }
     break;
   }
+  if constexpr (FUSED) {
+    __shared__ FinishSmem<256> sm;
+    if (!last_cta(done)) return;
+    for (int s = 0; s < S; ++s) finish_sequence(sm, part, off, s, T, E, k, lc, EP, out, err);
+    __threadfence_block();
+    __syncthreads();
+    finish_totals(sm, S, out);
+  }
 }
 
-// The slots of a sequence [lo, hi) in order: the warps of a CTA it covers in
-// part, one per CTA it covers whole, the warps of the last CTA in part.
-struct SeqSlots {
-  int s, first, nh, jm, nm, tail, nt;
-  __device__ SeqSlots(int s_, int lo, int hi, int T, int C) : s(s_) {
-    first = nh = jm = nm = tail = nt = 0;
-    if (lo >= hi) return;
-    const int CC = kWarps * C;
-    const int j0 = lo / CC, j1 = (hi - 1) / CC;
-    const bool from = lo == j0 * CC;
-    const bool upto = hi >= (int)min((long long)T, (long long)(j1 + 1) * CC);
-    first = lo / C;
-    if (j0 == j1 && !(from && upto)) {
-      nh = (hi - 1) / C - first + 1;
-      return;
-    }
-    jm = from ? j0 : j0 + 1;
-    nh = from ? 0 : (j0 + 1) * kWarps - first;
-    nm = (upto ? j1 + 1 : j1) - jm;
-    tail = j1 * kWarps;
-    nt = upto ? 0 : (hi - 1) / C - tail + 1;
-  }
-  __device__ int count() const { return nh + nm + nt; }
-  __device__ size_t operator()(int i) const {
-    const int w = i < nh ? first + i : i < nh + nm ? kWarps * (jm + i - nh) : tail + (i - nh - nm);
-    return (size_t)w + s;
-  }
-};
-
-// Sum over the CTA's 256 threads in a fixed order; every thread gets it.
-template <typename V>
-__device__ __forceinline__ V block_sum(V v, V* buf) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  V r = 0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) r += buf[w];
-  __syncthreads();
-  return r;
-}
-
-// One CTA per sequence (strided): counts, P, n and the sequence's terms of
-// both losses; the last CTA to finish adds the sequences.
-__global__ void __launch_bounds__(256)
+// One CTA per sequence (strided); the last CTA to finish adds the sequences.
+// NT threads: 1024 where the sequences are fewer than the SMs (and so may be
+// long, with a slot for every 64 tokens or more), else 256, several CTAs an SM.
+template <int NT>
+__global__ void __launch_bounds__(NT)
     balance_finish_kernel(BalanceParts part, const int32_t* __restrict__ off, int T, int E, int k,
-                          int S, int C, int EP, int32_t* __restrict__ counts,
-                          float* __restrict__ prob_mean, int32_t* tokens, float* losses,
-                          double* seq_terms, unsigned* done, int32_t* err) {
+                          int S, int lc, int EP, BalanceOut out, unsigned* done, int32_t* err) {
   pdl_wait_and_release();
-  __shared__ double sp[256];
-  __shared__ int32_t sc[256];
-  __shared__ double bufd[8];
-  __shared__ int32_t bufi[8];
-  __shared__ bool last;
-  const int tid = threadIdx.x;
-  const int ng = 256 / EP, e = tid % EP, gi = tid / EP;   // ng groups walk the slots
-  for (int s = blockIdx.x; s < S; s += gridDim.x) {
-    if (off != nullptr && tid == 0 &&
-        (off[s] < 0 || off[s + 1] < off[s] || off[s + 1] > T))
-      report_error(err, kDevBadOffsets);
-    int lo, hi;
-    seq_bounds(off, s, T, lo, hi);
-    const SeqSlots slots(s, lo, hi, T, C);
-    const int ni = slots.count();
-    double p = 0.0, z = 0.0;
-    int c = 0, n = 0;
-    if (e < E) {
-      for (int i = gi; i < ni; i += 4 * ng) {
-        float pv[4];
-        int cv[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool in = i + u * ng < ni;
-          const size_t at = in ? slots(i + u * ng) * E + e : 0;
-          pv[u] = in ? part.p[at] : 0.f;
-          cv[u] = in ? part.c[at] : 0;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          p += (double)pv[u];
-          c += cv[u];
-        }
-      }
-    }
-    for (int i = tid; i < ni; i += 256) {
-      const size_t at = slots(i);
-      n += part.n[at];
-      z += (double)part.z[at];
-    }
-    sp[tid] = p;
-    sc[tid] = c;
-    n = block_sum(n, bufi);   // (also orders sp and sc)
-    z = block_sum(z, bufd);
-    double term = 0.0;
-    if (tid < E) {
-      p = 0.0;
-      c = 0;
-      for (int j = 0; j < ng; ++j) {
-        p += sp[j * EP + tid];
-        c += sc[j * EP + tid];
-      }
-      const double P = n > 0 ? p / (double)n : 0.0;
-      counts[(size_t)s * E + tid] = c;
-      prob_mean[(size_t)s * E + tid] = (float)P;
-      if (n > 0) term = (double)c / ((double)n * k) * P;
-    }
-    term = block_sum(term, bufd);
-    if (tid == 0) {
-      tokens[s] = n;
-      seq_terms[2 * (size_t)s] = term * E;
-      seq_terms[2 * (size_t)s + 1] = z;
-    }
-  }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atom_add_acq_rel_gpu(done, 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  double b = 0.0, z = 0.0;
-  int n = 0, live = 0;
-  for (int s = tid; s < S; s += 256) {
-    const int ns = __ldcg(tokens + s);
-    b += __ldcg(seq_terms + 2 * (size_t)s);
-    z += __ldcg(seq_terms + 2 * (size_t)s + 1);
-    n += ns;
-    live += ns > 0;
-  }
-  b = block_sum(b, bufd);
-  z = block_sum(z, bufd);
-  n = block_sum(n, bufi);
-  live = block_sum(live, bufi);
-  if (tid == 0) {
-    losses[0] = live > 0 ? (float)(b / (double)live) : 0.f;
-    losses[1] = n > 0 ? (float)(z / (double)n) : 0.f;
-    tokens[S] = n;
-    tokens[S + 1] = live;
-    *done = 0;
-  }
+  __shared__ FinishSmem<NT> sm;
+  for (int s = blockIdx.x; s < S; s += gridDim.x)
+    finish_sequence(sm, part, off, s, T, E, k, lc, EP, out, err);
+  if (last_cta(done)) finish_totals(sm, S, out);
 }
 
-// The gradient: each warp owns C tokens and walks the sequences that meet
-// them; a sequence's a_se are in the lanes' registers.
-template <int G, int Q>
-__global__ void __launch_bounds__(256)
+template <typename L>
+__global__ void __launch_bounds__(256, 4)
     balance_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ off,
                             const uint8_t* __restrict__ mask, const int32_t* __restrict__ counts,
                             const int32_t* __restrict__ tokens, const float* __restrict__ dlosses,
-                            int T, int E, int k, int S, int C, float* __restrict__ dlogits,
+                            int T, int E, int k, int S, int lc, float* __restrict__ dlogits,
                             int32_t* err) {
   pdl_wait_and_release();
-  constexpr int W = 32 / G;
+  constexpr int G = L::G, W = L::W, NV = L::NV;
   const int lane = threadIdx.x & 31, g = lane / G, gl = lane % G;
   const int gw = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t0 = (int)min((long long)T, (long long)gw * C);
-  const int t1 = (int)min((long long)T, (long long)t0 + C);
+  const int t0 = (int)min((long long)T, (long long)gw << lc);
+  const int t1 = (int)min((long long)T, (long long)t0 + (1 << lc));
   if (t0 >= t1) return;
+  float nxt[NV];
+  load_logits<L>(logits, t0 + g, t0 + g < t1, E, gl, nxt);
   const int N = __ldg(tokens + S), live = __ldg(tokens + S + 1);
   const float dz = N > 0 ? (float)(2.0 * (double)__ldg(dlosses + 1) / (double)N) : 0.f;
   const double db = live > 0 ? (double)__ldg(dlosses) * E / (double)live : 0.0;
@@ -419,62 +554,68 @@ __global__ void __launch_bounds__(256)
     if (b >= e1) continue;
     const int n = __ldg(tokens + s);
     const double w = n > 0 ? db / ((double)n * (double)n * (double)k) : 0.0;
-    float a[Q];
+    float a[NV];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int e = gl + G * q;
-      a[q] = e < E ? (float)(w * (double)__ldg(counts + (size_t)s * E + e)) : 0.f;
+    for (int i = 0; i < NV; ++i) {
+      const int e = L::expert(gl, i);
+      a[i] = e < E ? (float)(w * (double)__ldg(counts + (size_t)s * E + e)) : 0.f;
     }
-    float nxt[Q];
-    bool nact = b + g < e1 && (mask == nullptr || mask[b + g] != 0);
-    load_logits<G, Q>(logits, b + g, nact, E, gl, nxt);
+    bool nact = b + g < e1 && (mask == nullptr || __ldg(mask + b + g) != 0);
+    if (b != t0) load_logits<L>(logits, b + g, b + g < e1, E, gl, nxt);
     for (int tb = b; tb < e1; tb += W) {
-      float L[Q], inv, lse;
+      float v[NV], inv, lse;
 #pragma unroll
-      for (int q = 0; q < Q; ++q) L[q] = nxt[q];
+      for (int i = 0; i < NV; ++i) v[i] = nxt[i];
       const bool act = nact;
       const int t = tb + g, tn = t + W;
-      nact = tn < e1 && (mask == nullptr || mask[tn] != 0);
-      load_logits<G, Q>(logits, tn, nact, E, gl, nxt);
-      softmax_terms<G, Q>(L, act, inv, lse);
+      nact = tn < e1 && (mask == nullptr || __ldg(mask + tn) != 0);
+      load_logits<L>(logits, tn, tn < e1, E, gl, nxt);
+      softmax_terms<L>(v, act, inv, lse);
       float pa = 0.f;
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        L[q] *= inv;
-        pa = fmaf(L[q], a[q], pa);
+      for (int i = 0; i < NV; ++i) {
+        v[i] *= inv;
+        pa = fmaf(v[i], a[i], pa);
       }
-      pa = group_sum<G>(pa);
-      if (t < e1) {
-        float* out = dlogits + (size_t)t * E;
+      pa = dz * lse - group_sum<G>(pa);
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-          if (gl + G * q < E) out[gl + G * q] = act ? L[q] * (a[q] - pa + dz * lse) : 0.f;
-      }
+      for (int i = 0; i < NV; ++i) v[i] = act ? v[i] * (a[i] + pa) : 0.f;
+      if (t < e1) store_values<L>(dlogits + (size_t)t * E, E, gl, v);
     }
   }
 }
 
-// Tokens of a warp: the fewest (8, 16, ...) that give at most 32 warps to
-// each of 148 SMs.
-int chunk_tokens(int T) {
-  int C = 8;
-  while (ceil_div(T, C) > 148 * 32 && C < (1 << 20)) C *= 2;
-  return C;
+// log2 of a warp's tokens C: the fewest (8, 16, ...) that give at most 32
+// warps to each of 148 SMs.
+int chunk_log(int T) {
+  int lc = 3;
+  while ((T >> lc) >= 148 * 32 && lc < 20) ++lc;
+  return lc;
 }
 
-// Calls f<G, Q>() for E experts.
+// Calls f with the lane layout for E experts; vec: E a multiple of 4 and every
+// row of fp32 values 16-byte aligned.  At most 16 values a lane, so that a
+// token's, the next one's and the sums stay in registers.
 template <typename F>
-cudaError_t by_width(int E, F&& f) {
-  using std::integral_constant;
-#define MOE_WIDTH(G, Q) f(integral_constant<int, G>{}, integral_constant<int, Q>{})
-  if (E <= 4) return MOE_WIDTH(4, 1);
-  if (E <= 8) return MOE_WIDTH(8, 1);
-  if (E <= 16) return MOE_WIDTH(16, 1);
-  if (E <= 32) return MOE_WIDTH(32, 1);
-  if (E <= 64) return MOE_WIDTH(32, 2);
-  if (E <= 128) return MOE_WIDTH(32, 4);
-  return MOE_WIDTH(32, 8);
-#undef MOE_WIDTH
+cudaError_t by_width(int E, bool vec, F&& f) {
+  if (vec) {
+    if (E <= 4) return f(Lanes<1, 4, true>{});
+    if (E <= 8) return f(Lanes<2, 4, true>{});
+    if (E <= 16) return f(Lanes<4, 4, true>{});
+    if (E <= 32) return f(Lanes<8, 4, true>{});
+    if (E <= 64) return f(Lanes<8, 8, true>{});
+    if (E <= 128) return f(Lanes<8, 16, true>{});
+    return f(Lanes<16, 16, true>{});
+  }
+  if (E <= 4) return f(Lanes<4, 1, false>{});
+  if (E <= 16) return f(Lanes<16, 1, false>{});
+  if (E <= 64) return f(Lanes<32, 2, false>{});
+  return f(Lanes<32, 8, false>{});
+}
+
+bool vector_rows(int E, const void* a, const void* b) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b);
+  return E % 4 == 0 && (at & 15u) == 0;
 }
 
 }  // namespace
@@ -487,7 +628,7 @@ BalanceLayout balance_layout(const moe_config_t& c, int S) {
     off += (bytes + 255) / 256 * 256;
     return o;
   };
-  const size_t slots = (size_t)ceil_div(c.T, chunk_tokens(c.T)) + kWarps + (size_t)S;
+  const size_t slots = (size_t)ceil_div(c.T, 1 << chunk_log(c.T)) + kWarps + (size_t)S;
   L.ctrl = take(256);
   L.p = take(slots * c.E * 4);
   L.c = take(slots * c.E * 4);
@@ -509,20 +650,27 @@ cudaError_t launch_balance_loss(const moe_config_t& c, int S, const int32_t* off
   const BalanceParts part{
       reinterpret_cast<float*>(base + L.p), reinterpret_cast<int32_t*>(base + L.c),
       reinterpret_cast<int32_t*>(base + L.n), reinterpret_cast<float*>(base + L.z)};
-  const int C = chunk_tokens(c.T);
-  if (c.T > 0) {
-    const cudaError_t e = by_width(c.E, [&](auto G, auto Q) {
-      return launch_kernel(balance_partial_kernel<decltype(G)::value, decltype(Q)::value>,
-                           ceil_div(c.T, kWarps * C), 256, 0, s, 0, logits, idx, off, mask, c.T,
-                           c.E, c.top_k, S, C, part, err);
-    });
-    if (e != cudaSuccess) return e;
-  }
+  const BalanceOut out{counts, prob_mean, tokens, losses,
+                       reinterpret_cast<double*>(base + L.terms)};
+  const int lc = chunk_log(c.T);
   int EP = 8;
   while (EP < c.E) EP *= 2;
-  return launch_kernel(balance_finish_kernel, std::min(S, device_sm_count() * 8), 256, 0, s, 0,
-                       part, off, c.T, c.E, c.top_k, S, C, EP, counts, prob_mean, tokens, losses,
-                       reinterpret_cast<double*>(base + L.terms), done, err);
+  const int grid = ceil_div(c.T, kWarps << lc);
+  const bool fused = grid > 0 && grid <= 16 && S <= 4;
+  if (grid > 0) {
+    const cudaError_t e = by_width(c.E, vector_rows(c.E, logits, nullptr), [&](auto lanes) {
+      using W = decltype(lanes);
+      const auto kern =
+          fused ? balance_partial_kernel<W, true> : balance_partial_kernel<W, false>;
+      return launch_kernel(kern, grid, 256, 0, s, 0, logits, idx, off, mask, c.T, c.E, c.top_k, S,
+                           lc, part, EP, out, done, err);
+    });
+    if (e != cudaSuccess || fused) return e;
+  }
+  const bool few = S < device_sm_count();
+  return launch_kernel(few ? balance_finish_kernel<1024> : balance_finish_kernel<256>,
+                       std::min(S, device_sm_count() * 4), few ? 1024 : 256, 0, s, 0, part, off,
+                       c.T, c.E, c.top_k, S, lc, EP, out, done, err);
 }
 
 cudaError_t launch_balance_loss_backward(const moe_config_t& c, int S, const int32_t* off,
@@ -531,12 +679,12 @@ cudaError_t launch_balance_loss_backward(const moe_config_t& c, int S, const int
                                          const float* dlosses, float* dlogits, void* ws,
                                          cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  const int C = chunk_tokens(c.T);
+  const int lc = chunk_log(c.T);
   int32_t* err = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + balance_layout(c, S).ctrl);
-  return by_width(c.E, [&](auto G, auto Q) {
-    return launch_kernel(balance_backward_kernel<decltype(G)::value, decltype(Q)::value>,
-                         ceil_div(c.T, kWarps * C), 256, 0, s, 0, logits, off, mask, counts,
-                         tokens, dlosses, c.T, c.E, c.top_k, S, C, dlogits, err);
+  return by_width(c.E, vector_rows(c.E, logits, dlogits), [&](auto lanes) {
+    return launch_kernel(balance_backward_kernel<decltype(lanes)>, ceil_div(c.T, kWarps << lc), 256,
+                         0, s, 0, logits, off, mask, counts, tokens, dlosses, c.T, c.E, c.top_k, S,
+                         lc, dlogits, err);
   });
 }
 

@@ -13,6 +13,8 @@
 // orders are those of combine.cu and backward.cu: "Mixture-of-Experts Routing
 // - LLM Internals" (mlgrind.dev), Algorithm 3.  fp32 throughout, one rounding
 // to the layer's dtype; all three are bound by HBM.
+#include <type_traits>
+
 #include "dropout.cuh"
 #include "moe_device.cuh"
 #include "moe_internal.h"
@@ -51,121 +53,131 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One warp per token, 8 columns a lane step; a dropped slot adds nothing.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    combine_dropout_kernel(const float* __restrict__ y_perm, const int32_t* __restrict__ dest,
-                           const float* __restrict__ gates, const T* residual, T* out, int rows,
-                           int k, int d_out, DropArgs d) {
-  pdl_wait_and_release();
-  const uint64_t offset = drop_offset(d);
-  const int lane = threadIdx.x & 31;
-  const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int nw = (gridDim.x * blockDim.x) >> 5;
-  const int nvec = d_out / 8;
-  for (int t = gw; t < rows; t += nw) {
-    int dl = -1;
-    float gl = 0.f;
-    if (lane < k) {
-      dl = dest[(size_t)t * k + lane];
-      gl = gates[(size_t)t * k + lane];
-    }
-    int dj[8];
-    float gj[8];
+// The combine's two directions.  W warps of a CTA share a token (8 / W tokens
+// a CTA; W by d_out, so that a warp has about four steps of 32 x 8 columns and
+// the grid has enough CTAs to end evenly).  K = top_k rounded up to 1, 2, 4 or
+// 8: a token's rows and gates take K registers; rows are loaded KB = min(K, 4)
+// at a time, all before the first is used.  A dropped slot adds nothing.
+constexpr int kSlotBatch = 4;
+
+template <int K>
+__device__ __forceinline__ void load_slots(const int32_t* __restrict__ dest,
+                                           const float* __restrict__ gates, int t, int k, bool in,
+                                           int (&dj)[K], float (&gj)[K]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dj[j] = __shfl_sync(0xffffffffu, dl, j);
-      gj[j] = __shfl_sync(0xffffffffu, gl, j);
-    }
-    const uint64_t blk = d.block0 + (uint64_t)t * nvec;
-#pragma unroll 2
-    for (int v = lane; v < nvec; v += 32) {
-      float acc[8], r[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = r[i] = 0.f;
-      if (residual != nullptr) load_row8(residual + ((size_t)t * nvec + v) * 8, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j < k && dj[j] >= 0) {
-          const float4* src = reinterpret_cast<const float4*>(y_perm + (size_t)dj[j] * d_out) + 2 * v;
-          const float4 a = __ldg(src), b = __ldg(src + 1);
-          acc[0] = fmaf(gj[j], a.x, acc[0]);
-          acc[1] = fmaf(gj[j], a.y, acc[1]);
-          acc[2] = fmaf(gj[j], a.z, acc[2]);
-          acc[3] = fmaf(gj[j], a.w, acc[3]);
-          acc[4] = fmaf(gj[j], b.x, acc[4]);
-          acc[5] = fmaf(gj[j], b.y, acc[5]);
-          acc[6] = fmaf(gj[j], b.z, acc[6]);
-          acc[7] = fmaf(gj[j], b.w, acc[7]);
-        }
-      }
-      const uint32_t keep = drop_keep8(d, offset, blk + v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = r[i] + ((keep >> i) & 1u ? acc[i] * d.scale : 0.f);
-      store_row8(out + ((size_t)t * nvec + v) * 8, acc);
-    }
+  for (int j = 0; j < K; ++j) {
+    dj[j] = in && j < k ? __ldg(dest + (size_t)t * k + j) : -1;
+    gj[j] = in && j < k ? __ldg(gates + (size_t)t * k + j) : 0.f;
   }
 }
 
-// One warp per token; dgates as in backward.cu: per lane in column order,
-// then a fixed butterfly over the warp.
-template <typename T>
-__global__ void __launch_bounds__(256)
+template <typename T, int K>
+__global__ void __launch_bounds__(256, K <= 2 ? 4 : 3)
+    combine_dropout_kernel(const float* __restrict__ y_perm, const int32_t* __restrict__ dest,
+                           const float* __restrict__ gates, const T* residual, T* out, int rows,
+                           int k, int d_out, int W, DropArgs d) {
+  pdl_wait_and_release();
+  constexpr int KB = K < kSlotBatch ? K : kSlotBatch;
+  const uint64_t offset = drop_offset(d);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (8 / W) + warp / W;
+  if (t >= rows) return;
+  const int nvec = d_out / 8;
+  int dj[K];
+  float gj[K];
+  load_slots<K>(dest, gates, t, k, true, dj, gj);
+  const size_t row = (size_t)t * nvec;
+  for (int v = warp % W * 32 + lane; v < nvec; v += 32 * W) {
+    float r[8], acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = r[i] = 0.f;
+    if (residual != nullptr) load_row8(residual + (row + v) * 8, r);
+    uint32_t keep = 0;
+#pragma unroll
+    for (int j0 = 0; j0 < K; j0 += KB) {
+      float y[KB][8];
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        if (dj[j0 + j] >= 0)
+          load_row8_stream(y_perm + ((size_t)dj[j0 + j] * nvec + v) * 8, y[j]);
+      if (j0 == 0) keep = drop_keep8(d, offset, d.block0 + row + v);
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        if (dj[j0 + j] >= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = fmaf(gj[j0 + j], y[j][i], acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = r[i] + ((keep >> i) & 1u ? acc[i] * d.scale : 0.f);
+    store_row8(out + (row + v) * 8, acc);
+  }
+}
+
+// dgates: per lane in column order, a fixed butterfly over the warp, the
+// token's W warps in order.
+template <typename T, int K>
+__global__ void __launch_bounds__(256, K <= 2 ? 4 : 3)
     combine_dropout_backward_kernel(const T* __restrict__ dy, const float* __restrict__ y_perm,
                                     const int32_t* __restrict__ dest,
                                     const float* __restrict__ gates, float* __restrict__ dy_perm,
-                                    float* __restrict__ dgates, int rows, int k, int d_out,
+                                    float* __restrict__ dgates, int rows, int k, int d_out, int W,
                                     DropArgs d) {
   pdl_wait_and_release();
+  constexpr int KB = K < kSlotBatch ? K : kSlotBatch;
+  __shared__ float red[8][K];
   const uint64_t offset = drop_offset(d);
-  const int lane = threadIdx.x & 31;
-  const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int nw = (gridDim.x * blockDim.x) >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (8 / W) + warp / W;
+  const bool in = t < rows;
   const int nvec = d_out / 8;
-  for (int t = gw; t < rows; t += nw) {
-    int dl = -1;
-    float gl = 0.f;
-    if (lane < k) {
-      dl = dest[(size_t)t * k + lane];
-      gl = gates[(size_t)t * k + lane];
-    }
-    int dj[8];
-    float gj[8], part[8];
+  int dj[K];
+  float gj[K], part[K];
+  load_slots<K>(dest, gates, t, k, in, dj, gj);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dj[j] = __shfl_sync(0xffffffffu, dl, j);
-      gj[j] = __shfl_sync(0xffffffffu, gl, j);
-      part[j] = 0.f;
-    }
-    const uint64_t blk = d.block0 + (uint64_t)t * nvec;
-    for (int v = lane; v < nvec; v += 32) {
-      float g8[8];
-      load_row8(dy + ((size_t)t * nvec + v) * 8, g8);
-      const uint32_t keep = drop_keep8(d, offset, blk + v);
+  for (int j = 0; j < K; ++j) part[j] = 0.f;
+  const size_t row = (size_t)t * nvec;
+  for (int v = warp % W * 32 + lane; in && v < nvec; v += 32 * W) {
+    float g8[8];
+    load_row8(dy + (row + v) * 8, g8);
+    uint32_t keep = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g8[i] = (keep >> i) & 1u ? g8[i] * d.scale : 0.f;
+    for (int j0 = 0; j0 < K; j0 += KB) {
+      float y[KB][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j < k && dj[j] >= 0) {
-          float y8[8];
-          load_row8(y_perm + (size_t)dj[j] * d_out + (size_t)v * 8, y8);
+      for (int j = 0; j < KB; ++j)
+        if (dj[j0 + j] >= 0)
+          load_row8_stream(y_perm + ((size_t)dj[j0 + j] * nvec + v) * 8, y[j]);
+      if (j0 == 0) {
+        keep = drop_keep8(d, offset, d.block0 + row + v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((keep >> i) & 1u) part[j] = fmaf(g8[i], y8[i], part[j]);
-          float4* o = reinterpret_cast<float4*>(dy_perm + (size_t)dj[j] * d_out + (size_t)v * 8);
-          o[0] = make_float4(gj[j] * g8[0], gj[j] * g8[1], gj[j] * g8[2], gj[j] * g8[3]);
-          o[1] = make_float4(gj[j] * g8[4], gj[j] * g8[5], gj[j] * g8[6], gj[j] * g8[7]);
-        }
+        for (int i = 0; i < 8; ++i) g8[i] = (keep >> i) & 1u ? g8[i] * d.scale : 0.f;
       }
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        if (dj[j0 + j] >= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if ((keep >> i) & 1u) part[j0 + j] = fmaf(g8[i], y[j][i], part[j0 + j]);
+            y[j][i] = gj[j0 + j] * g8[i];
+          }
+          store_row8_stream(dy_perm + ((size_t)dj[j0 + j] * nvec + v) * 8, y[j]);
+        }
     }
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < K; ++j) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < k && lane == j) dgates[(size_t)t * k + j] = dj[j] >= 0 ? part[j] : 0.f;
+    for (int o = 16; o > 0; o >>= 1) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
+    if (lane == 0) red[warp][j] = part[j];
+  }
+  if (W > 1) __syncthreads();
+  else __syncwarp();
+  if (in && warp % W == 0 && lane < k) {
+    float v = red[warp][lane];
+    for (int w = 1; w < W; ++w) v += red[warp + w][lane];
+    // a dropped slot's sum is 0
+    dgates[(size_t)t * k + lane] = v;
   }
 }
 
@@ -191,18 +203,38 @@ cudaError_t launch_dropout(long long rows, int width, bool bf16, const void* x, 
               : run_dropout<float>(x, add, out, nblk, d, s);
 }
 
+namespace {
+
+// Calls f(K) with top_k rounded up to 1, 2, 4 or 8.
+template <typename F>
+cudaError_t by_slots(int k, F&& f) {
+  using std::integral_constant;
+  if (k == 1) return f(integral_constant<int, 1>{});
+  if (k == 2) return f(integral_constant<int, 2>{});
+  if (k <= 4) return f(integral_constant<int, 4>{});
+  return f(integral_constant<int, 8>{});
+}
+
+// Warps a token: four steps of 256 columns each, as far as d_out gives them.
+int token_warps(int d_out) { return d_out >= 8192 ? 8 : d_out >= 4096 ? 4 : d_out >= 2048 ? 2 : 1; }
+
+}  // namespace
+
 cudaError_t launch_combine_dropout(const moe_config_t& c, const float* y_perm, const int32_t* dest,
                                    const float* gates, const void* residual, void* out,
                                    const DropArgs& d, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  const int blocks = std::min(ceil_div(c.T, 8), device_sm_count() * 16);
-  if (c.act_dtype == MOE_BF16)
-    return launch_kernel(combine_dropout_kernel<__nv_bfloat16>, blocks, 256, 0, s, 0, y_perm, dest,
-                         gates, static_cast<const __nv_bfloat16*>(residual),
-                         static_cast<__nv_bfloat16*>(out), c.T, c.top_k, c.d_out, d);
-  return launch_kernel(combine_dropout_kernel<float>, blocks, 256, 0, s, 0, y_perm, dest, gates,
-                       static_cast<const float*>(residual), static_cast<float*>(out), c.T, c.top_k,
-                       c.d_out, d);
+  auto run = [&](auto* o) {
+    using T = std::remove_pointer_t<decltype(o)>;
+    const int W = token_warps(c.d_out);
+    return by_slots(c.top_k, [&](auto K) {
+      return launch_kernel(combine_dropout_kernel<T, decltype(K)::value>, ceil_div(c.T, 8 / W),
+                           256, 0, s, 0, y_perm, dest, gates, static_cast<const T*>(residual), o,
+                           c.T, c.top_k, c.d_out, W, d);
+    });
+  };
+  return c.act_dtype == MOE_BF16 ? run(static_cast<__nv_bfloat16*>(out))
+                                 : run(static_cast<float*>(out));
 }
 
 cudaError_t launch_combine_dropout_backward(const moe_config_t& c, const void* dy,
@@ -210,14 +242,18 @@ cudaError_t launch_combine_dropout_backward(const moe_config_t& c, const void* d
                                             const float* gates, float* dy_perm, float* dgates,
                                             const DropArgs& d, cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  const int blocks = std::min(ceil_div(c.T, 8), device_sm_count() * 16);
-  if (c.act_dtype == MOE_BF16)
-    return launch_kernel(combine_dropout_backward_kernel<__nv_bfloat16>, blocks, 256, 0, s, 0,
-                         static_cast<const __nv_bfloat16*>(dy), y_perm, dest, gates, dy_perm,
-                         dgates, c.T, c.top_k, c.d_out, d);
-  return launch_kernel(combine_dropout_backward_kernel<float>, blocks, 256, 0, s, 0,
-                       static_cast<const float*>(dy), y_perm, dest, gates, dy_perm, dgates, c.T,
-                       c.top_k, c.d_out, d);
+  auto run = [&](auto* g) {
+    using T = std::remove_pointer_t<decltype(g)>;
+    const int W = token_warps(c.d_out);
+    return by_slots(c.top_k, [&](auto K) {
+      return launch_kernel(
+          combine_dropout_backward_kernel<std::remove_const_t<T>, decltype(K)::value>,
+          ceil_div(c.T, 8 / W), 256, 0, s, 0, g, y_perm, dest, gates, dy_perm, dgates, c.T,
+          c.top_k, c.d_out, W, d);
+    });
+  };
+  return c.act_dtype == MOE_BF16 ? run(static_cast<const __nv_bfloat16*>(dy))
+                                 : run(static_cast<const float*>(dy));
 }
 
 }  // namespace moe

@@ -77,4 +77,16 @@ __device__ __forceinline__ void store_row8(float* p, const float (&a)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(a[4], a[5], a[6], a[7]);
 }
 
+// fp32 rows read once and written once: past L1, and the first to leave L2.
+__device__ __forceinline__ void load_row8_stream(const float* p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store_row8_stream(float* p, const float (&a)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(a[0], a[1], a[2], a[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(a[4], a[5], a[6], a[7]));
+}
+
 }  // namespace moe
