@@ -81,104 +81,91 @@ __device__ __forceinline__ uint32_t tile_at(int row, int c) {
   return (uint32_t)(row * CPR + (c ^ sw)) * 16u;
 }
 
-// A value as a sum of bf16 terms.
+// Four values as a sum of N bf16 terms each: t[i] holds the four i-th terms.
 template <int N>
-__device__ __forceinline__ void split_bf16(float v, __nv_bfloat16 (&t)[N]) {
+__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&t)[N]) {
+  float a = v[0], b = v[1], c = v[2], d = v[3];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    t[i] = __float2bfloat16(v);
-    v -= __bfloat162float(t[i]);
+    t[i] = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+    a -= __uint_as_float(t[i].x << 16);
+    b -= __uint_as_float(t[i].x & 0xFFFF0000u);
+    c -= __uint_as_float(t[i].y << 16);
+    d -= __uint_as_float(t[i].y & 0xFFFF0000u);
   }
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint2 v) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y)
+               : "memory");
 }
 
 // ------------------------------------------------------------------- plan --
 
 constexpr int kPlanThreads = 1024;
 
-// CTA g writes group g: adapter g's rows, or (g = n) the rows without one.
+// CTA g writes group g: adapter g's rows, or (g = n) the rows without one.  Each
+// warp owns a range of tokens and counts those of earlier groups and of its
+// own; after one exchange it writes its rows in token order.  A group's tiles
+// have the slots from offsets[g] / TM + g on, which no other group's have, so
+// that nothing needs the other groups' counts; slots left over hold no rows.
 __global__ void __launch_bounds__(kPlanThreads)
     adapter_plan_kernel(const int32_t* __restrict__ ids, int T, int n, int TM, int32_t* header,
                         int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
                         int4* __restrict__ tiles, int32_t* err) {
   pdl_wait_and_release();
-  __shared__ int32_t hist[kAdapterMaxCount + 1];
-  __shared__ int32_t wsum[32], wsum2[32];
-  __shared__ int32_t s_row0, s_tile0, s_run;
+  __shared__ int32_t s_less[32], s_mine[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x;
-  auto group_of = [&](int t) {
+  const int per = ceil_div_dev(ceil_div_dev(T, 32), 32) * 32;   // T <= 2^30
+  const int t0 = (int)min((long long)T, (long long)warp * per), t1 = min(T, t0 + per);
+  auto group = [&](int t) {
     const int a = __ldg(ids + t);
-    return a < 0 || a >= n ? n : a;
+    return (unsigned)a >= (unsigned)n ? n : a;
   };
-  for (int i = tid; i <= n; i += kPlanThreads) hist[i] = 0;
-  __syncthreads();
-  for (int t0 = 0; t0 < T; t0 += kPlanThreads) {
-    const int t = t0 + tid;
-    const int a = t < T ? group_of(t) : -1;
-    // lanes of the same group add once
-    const unsigned peers = __match_any_sync(0xffffffffu, a);
-    if (a >= 0 && (peers & lanemask_lt()) == 0) atomicAdd(&hist[a], __popc(peers));
-    if (g == 0 && t < T && __ldg(ids + t) >= n) report_error(err, kDevBadExpertIndex);
+  int less = 0, mine = 0;
+  bool bad = false;
+#pragma unroll 8
+  for (int t = t0 + lane; t < t1; t += 32) {
+    const int a = __ldg(ids + t);
+    const int q = (unsigned)a >= (unsigned)n ? n : a;
+    less += q < g;
+    mine += q == g;
+    bad |= a >= n;
   }
-  __syncthreads();
-  // rows and tiles before group g
-  int r = 0, q = 0;
-  for (int i = tid; i < g; i += kPlanThreads) {
-    r += hist[i];
-    q += (hist[i] + TM - 1) / TM;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    r += __shfl_xor_sync(0xffffffffu, r, o);
-    q += __shfl_xor_sync(0xffffffffu, q, o);
-  }
+  if (bad && g == 0) report_error(err, kDevBadExpertIndex);
+  less = __reduce_add_sync(0xffffffffu, less);
+  mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) {
-    wsum[warp] = r;
-    wsum2[warp] = q;
+    s_less[warp] = less;
+    s_mine[warp] = mine;
   }
   __syncthreads();
+  const int row0 = __reduce_add_sync(0xffffffffu, s_less[lane]);
+  const int cnt = __reduce_add_sync(0xffffffffu, s_mine[lane]);
   if (tid == 0) {
-    r = q = 0;
-    for (int w = 0; w < 32; ++w) {
-      r += wsum[w];
-      q += wsum2[w];
-    }
-    s_row0 = r;
-    s_tile0 = q;
-    s_run = 0;
-    offsets[g] = r;
+    offsets[g] = row0;
     if (g == n) {
       offsets[n + 1] = T;
       header[0] = T;
       header[1] = n;
-      header[2] = q + (hist[n] + TM - 1) / TM;
     }
   }
-  __syncthreads();
-  const int row0 = s_row0, tile0 = s_tile0, cnt = hist[g];
-  for (int i = tid; i * TM < cnt; i += kPlanThreads)
-    tiles[tile0 + i] = make_int4(g, row0 + i * TM, min(TM, cnt - i * TM), 0);
-  for (int t0 = 0; t0 < T; t0 += kPlanThreads) {
-    const int t = t0 + tid;
-    const bool mine = t < T && group_of(t) == g;
-    const unsigned b = __ballot_sync(0xffffffffu, mine);
-    __syncthreads();   // the last block's wsum has been read
-    if (lane == 0) wsum[warp] = __popc(b);
-    __syncthreads();
-    const int v = wsum[lane];
-    int before = lane < warp ? v : 0, all = v;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    if (mine) rows[row0 + s_run + before + __popc(b & lanemask_lt())] = t;
-    __syncthreads();
-    if (tid == 0) s_run += all;
+  const int slot0 = row0 / TM + g, nslots = (row0 + cnt) / TM + g + 1 - slot0;
+  for (int i = tid; i < nslots; i += kPlanThreads)
+    tiles[slot0 + i] = make_int4(g, row0 + i * TM, min(TM, max(0, cnt - i * TM)), 0);
+  if (mine == 0) return;
+  int at = row0 + __reduce_add_sync(0xffffffffu, lane < warp ? s_mine[lane] : 0);
+#pragma unroll 4
+  for (int t = t0; t < t1; t += 32) {
+    const bool in = t + lane < t1 && group(t + lane) == g;
+    const unsigned b = __ballot_sync(0xffffffffu, in);
+    if (in) rows[at + __popc(b & lanemask_lt())] = t + lane;
+    at += __popc(b);
   }
 }
 
 // --------------------------------------------------------------- low rank --
 
+// RP: the rank rounded up to 16, 32, 64 or 128; TM: rows of a tile.
 template <int RP, int TM, bool BWD>
 struct LowRank {
   static constexpr int KC = TM == 64 ? 64 : 128;      // input columns a stage
@@ -193,76 +180,100 @@ struct LowRank {
   static constexpr int OB = BWD ? 4 : 2;              // bytes of an output element
   static constexpr int S1 = TM * KC * 2 + KC * RP * 2;
   static constexpr int S2 = RP * NC * 2 + TM * NC * OB;
-  static constexpr int ST1 = S1 > 24 * 1024 ? 3 : 4;
-  static constexpr int ST2 = 3;
+  static constexpr int ST1 = TM == 16 ? 3 : 4;
+  static constexpr int ST2 = TM == 16 && RP > 32 ? 2 : 3;
+  // Few rows (decode): both products' first stages are loaded at once, from
+  // rings of their own.  Many rows: one ring, so that two to four CTAs fit an
+  // SM and one's input overlaps another's output.
+  static constexpr bool AHEAD = TM == 16;
   static constexpr int RED = WK > 1 ? WK * TM * RP * 4 : 0;
-  static constexpr int RING0 = ST1 * S1 > ST2 * S2 ? ST1 * S1 : ST2 * S2;
-  static constexpr int RING = RING0 > RED ? RING0 : RED;
+  static constexpr int R1 = ST1 * S1 > RED ? ST1 * S1 : RED;
+  static constexpr int R2 = ST2 * S2;
+  static constexpr int RING2 = AHEAD ? R1 : 0;        // where the second ring starts
+  static constexpr int RING = AHEAD ? R1 + R2 : (R1 > R2 ? R1 : R2);
   static constexpr int US = TERMS * TM * RP * 2;
   static constexpr int PART = TM * RP * 4;
   static constexpr int SMEM = RING + US + PART;
+  static constexpr int CTAS = 227 * 1024 / (SMEM + 1024 + TM * 4);   // an SM holds, by memory
 };
 
-// in (T, K) bf16; W1, W2 per adapter: forward A (K, r) and B (r, N), backward
-// B (r, K) and A (N, r); base (T, N) and out (T, N): bf16 forward, fp32
-// backward; base may be null (0) or out.  u (T, r) fp32 or null.
+struct LowRankArgs {
+  const __nv_bfloat16* in;    // (T, K)
+  const __nv_bfloat16* W1;    // per adapter: forward A (K, r), backward B (r, K)
+  const __nv_bfloat16* W2;    // per adapter: forward B (r, N), backward A (N, r)
+  const float* scale;
+  const void* base;           // (T, N), bf16 forward, fp32 backward; null (0) or out
+  void* out;                  // (T, N)
+  float* u;                   // forward: (T, r) out or null; backward: the forward's
+  __nv_bfloat16* up;          // backward: u's and v's three terms out, (T, 3, r)
+  __nv_bfloat16* vp;
+  const int32_t* header;
+  const int32_t* rows;
+  const int4* tiles;
+  int32_t* err;
+  int T, n, r, K, N;
+};
+
 template <int RP, int TM, bool BWD>
-__global__ void __launch_bounds__(256)
-    low_rank_kernel(const __nv_bfloat16* __restrict__ in, const __nv_bfloat16* __restrict__ W1,
-                    const __nv_bfloat16* __restrict__ W2, const float* __restrict__ scale,
-                    const void* base, void* out, float* __restrict__ u, int T, int n, int r, int K,
-                    int N, const int32_t* __restrict__ header, const int32_t* __restrict__ rows,
-                    const int4* __restrict__ tiles, int32_t* err) {
+__global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
   using L = LowRank<RP, TM, BWD>;
   pdl_wait_and_release();
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int32_t s_rows[TM];
-  const uint32_t ring = smem_u32(smem), us = ring + L::RING, part = us + L::US;
+  const uint32_t ring = smem_u32(smem), us = ring + L::RING;
   float* partp = reinterpret_cast<float*>(smem + L::RING + L::US);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t cs;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
   const int CS = (int)cs, cr = (int)cluster_cta_rank();
-  const int tile = blockIdx.x / CS;
-  if (__ldg(header) != T || __ldg(header + 1) != n) {   // the same for every CTA
-    if (tid == 0) report_error(err, kDevBadPlan);
+  const int hT = __ldg(g.header), hn = __ldg(g.header + 1);
+  const int4 tl = __ldg(g.tiles + blockIdx.x / CS);
+  const int r = g.r, K = g.K, N = g.N, a = tl.x, nrows = tl.z;
+  if (hT != g.T || hn != g.n) {   // the same for every CTA
+    if (tid == 0) report_error(g.err, kDevBadPlan);
     return;
   }
-  if (tile >= __ldg(header + 2)) return;                // the same for the cluster
-  const int4 tl = __ldg(tiles + tile);
-  const int a = tl.x, nrows = tl.z;
-  if (tid < TM) s_rows[tid] = tid < nrows ? __ldg(rows + tl.y + tid) : -1;
-  __syncthreads();
+  if (nrows == 0) return;         // the same for the cluster
+  // The token of tile row i, -1 behind the last.
+  auto token = [&](int i) { return i < nrows ? __ldg(g.rows + tl.y + i) : -1; };
   const int nn = ceil_div_dev(N, L::NC);
   const int n0 = (int)((long long)nn * cr / CS), n1 = (int)((long long)nn * (cr + 1) / CS);
-  if (a == n) {   // rows without an adapter: out = base
-    if (base == out) return;
-    constexpr int PV = 16 / L::OB;
-    const int v0 = n0 * L::NC / PV, v1 = min(n1 * L::NC, N) / PV, nv = v1 - v0;
-    for (int i = tid; i < nrows * nv; i += 256) {
-      const size_t at = (size_t)s_rows[i / nv] * (N / PV) + v0 + i % nv;
-      static_cast<uint4*>(out)[at] =
-          base != nullptr ? static_cast<const uint4*>(base)[at] : make_uint4(0, 0, 0, 0);
+  constexpr int PV = 16 / L::OB;           // output elements of 16 bytes
+  constexpr int BC = L::NC / PV;           // 16-byte pieces of a stage's output row
+  constexpr int BR = TM * BC / 256;        // output rows of a thread in a stage
+  int bt[BR];
+#pragma unroll
+  for (int i = 0; i < BR; ++i) bt[i] = token(tid / BC + i * (256 / BC));
+  if (a == g.n) {   // rows without an adapter: out = base
+    if (g.base == g.out) return;
+    for (int nc = n0; nc < n1; ++nc) {
+      const int col = nc * L::NC + tid % BC * PV;
+#pragma unroll
+      for (int i = 0; i < BR; ++i)
+        if (bt[i] >= 0 && col < N) {
+          const size_t at = ((size_t)bt[i] * N + col) / PV;
+          static_cast<uint4*>(g.out)[at] = g.base != nullptr
+                                               ? static_cast<const uint4*>(g.base)[at]
+                                               : make_uint4(0, 0, 0, 0);
+        }
     }
     return;
   }
-  const __nv_bfloat16* w1 = W1 + (size_t)a * K * r;
-  const __nv_bfloat16* w2 = W2 + (size_t)a * N * r;
+  const __nv_bfloat16* w1 = g.W1 + (size_t)a * K * r;
+  const __nv_bfloat16* w2 = g.W2 + (size_t)a * N * r;
 
-  // ---- first product: part = in[rows, slice] W1[slice, :] ----
+  // ---- loads ----
   const int nk = ceil_div_dev(K, L::KC);
   const int k0 = (int)((long long)nk * cr / CS), k1 = (int)((long long)nk * (cr + 1) / CS);
-  auto load1 = [&](int kc) {
-    const uint32_t xs = ring + (uint32_t)((kc - k0) % L::ST1) * L::S1;
-    const uint32_t ws = xs + TM * L::KC * 2;
-    constexpr int XC = L::KC / 8;
+  constexpr int XC = L::KC / 8;            // 16-byte pieces of a stage's input row
+  constexpr int XR = TM * XC / 256;        // input rows of a thread in a stage
+  const __nv_bfloat16* xrow[XR];
 #pragma unroll
-    for (int i = tid; i < TM * XC; i += 256) {
-      const int row = i / XC, c = i % XC, col = kc * L::KC + c * 8;
-      const int t = s_rows[row];
-      const bool ok = t >= 0 && col < K;
-      cp_async16(xs + tile_at<XC>(row, c), ok ? in + (size_t)t * K + col : in, ok);
-    }
+  for (int i = 0; i < XR; ++i) {
+    const int t = token(tid / XC + i * (256 / XC));
+    xrow[i] = t >= 0 ? g.in + (size_t)t * K : nullptr;
+  }
+  auto load_w1 = [&](int kc) {
+    const uint32_t ws = ring + (uint32_t)((kc - k0) % L::ST1) * L::S1 + TM * L::KC * 2;
     if (!BWD) {   // [k][j]
       constexpr int RC = RP / 8;
 #pragma unroll
@@ -280,57 +291,18 @@ __global__ void __launch_bounds__(256)
       }
     }
   };
-  const int wm = warp % L::WM, wk = (warp / L::WM) % L::WK, wn = warp / (L::WM * L::WK);
-  float acc[L::NT][4];
-#pragma unroll
-  for (int i = 0; i < L::NT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll
-  for (int i = 0; i < L::ST1 - 1; ++i) {
-    if (k0 + i < k1) load1(k0 + i);
-    cp_commit();
-  }
-  for (int kc = k0; kc < k1; ++kc) {
-    cp_wait<L::ST1 - 2>();
-    __syncthreads();
-    if (kc + L::ST1 - 1 < k1) load1(kc + L::ST1 - 1);
-    cp_commit();
+  auto load_x = [&](int kc) {
     const uint32_t xs = ring + (uint32_t)((kc - k0) % L::ST1) * L::S1;
-    const uint32_t ws = xs + TM * L::KC * 2;
-    float c[L::NT][4];
+    const int col = kc * L::KC + tid % XC * 8;
 #pragma unroll
-    for (int i = 0; i < L::NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
-#pragma unroll
-    for (int ks = wk; ks < L::KC / 16; ks += L::WK) {
-      uint32_t fa[4];
-      ldsm4(xs + tile_at<L::KC / 8>(wm * 16 + (lane & 15), ks * 2 + (lane >> 4)), fa);
-#pragma unroll
-      for (int p = 0; p < L::NT / 2; ++p) {
-        const int j0 = wn * (RP / L::WN) + p * 16;
-        uint32_t fb[4];
-        if (!BWD)
-          ldsm4_t(ws + tile_at<RP / 8>(ks * 16 + (lane & 15), j0 / 8 + (lane >> 4)), fb);
-        else
-          ldsm4(ws + tile_at<L::KC / 8>(j0 + (lane & 7) + (lane >> 4) * 8,
-                                        ks * 2 + ((lane >> 3) & 1)), fb);
-        mma16816(c[2 * p], fa, fb[0], fb[1]);
-        mma16816(c[2 * p + 1], fa, fb[2], fb[3]);
-      }
+    for (int i = 0; i < XR; ++i) {
+      const bool ok = xrow[i] != nullptr && col < K;
+      cp_async16(xs + tile_at<XC>(tid / XC + i * (256 / XC), tid % XC),
+                 ok ? xrow[i] + col : g.in, ok);
     }
-#pragma unroll
-    for (int i = 0; i < L::NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] += c[i][j];
-  }
-  cp_wait<0>();
-  __syncthreads();   // the ring is free
-
-  // ---- second product's loads ----
+  };
   auto load2 = [&](int nc) {
-    const uint32_t ws = ring + (uint32_t)((nc - n0) % L::ST2) * L::S2;
+    const uint32_t ws = ring + L::RING2 + (uint32_t)((nc - n0) % L::ST2) * L::S2;
     const uint32_t bs = ws + RP * L::NC * 2;
     if (!BWD) {   // [j][c]
       constexpr int CC = L::NC / 8;
@@ -349,53 +321,118 @@ __global__ void __launch_bounds__(256)
         cp_async16(ws + tile_at<RC>(row, c), ok ? w2 + (size_t)col * r + c * 8 : w2, ok);
       }
     }
-    constexpr int BC = L::NC * L::OB / 16;   // 16-byte pieces of a base row
-    constexpr int PV = 16 / L::OB;
+    const int col = nc * L::NC + tid % BC * PV;
 #pragma unroll
-    for (int i = tid; i < TM * BC; i += 256) {
-      const int row = i / BC, c = i % BC, col = nc * L::NC + c * PV;
-      const int t = s_rows[row];
-      const bool ok = t >= 0 && col < N && base != nullptr;
-      const uint8_t* src = static_cast<const uint8_t*>(base) + ((size_t)t * N + col) * L::OB;
-      cp_async16(bs + tile_at<BC>(row, c), ok ? src : reinterpret_cast<const uint8_t*>(w2), ok);
+    for (int i = 0; i < BR; ++i) {
+      const bool ok = bt[i] >= 0 && col < N && g.base != nullptr;
+      const uint8_t* src =
+          static_cast<const uint8_t*>(g.base) + ((size_t)(ok ? bt[i] : 0) * N + col) * L::OB;
+      cp_async16(bs + tile_at<BC>(tid / BC + i * (256 / BC), tid % BC),
+                 ok ? src : reinterpret_cast<const uint8_t*>(w2), ok);
     }
   };
+  // The second product's first stages; AHEAD, they belong to the last group
+  // that goes out before the first product.
   auto begin2 = [&]() {
 #pragma unroll
     for (int i = 0; i < L::ST2 - 1; ++i) {
       if (n0 + i < n1) load2(n0 + i);
-      cp_commit();
+      if (!L::AHEAD) cp_commit();
     }
   };
 
-  // ---- u: the warps' and then the CTAs' partial sums, in order ----
+  // ---- first product: part = in[rows, slice] W1[slice, :] ----
+  const int wm = warp % L::WM, wk = (warp / L::WM) % L::WK, wn = warp / (L::WM * L::WK);
+  float acc[L::NT][4];
+#pragma unroll
+  for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < L::ST1 - 1; ++i)
+    if (k0 + i < k1) load_w1(k0 + i);   // (needs no row: out before the rows are known)
+#pragma unroll
+  for (int i = 0; i < L::ST1 - 1; ++i) {
+    if (k0 + i < k1) load_x(k0 + i);
+    if (L::AHEAD && i == L::ST1 - 2) begin2();
+    cp_commit();
+  }
+  for (int kc = k0; kc < k1; ++kc) {
+    cp_wait<L::ST1 - 2>();
+    __syncthreads();
+    if (kc + L::ST1 - 1 < k1) {
+      load_w1(kc + L::ST1 - 1);
+      load_x(kc + L::ST1 - 1);
+    }
+    cp_commit();
+    const uint32_t xs = ring + (uint32_t)((kc - k0) % L::ST1) * L::S1;
+    const uint32_t ws = xs + TM * L::KC * 2;
+    float c[L::NT][4];
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
+#pragma unroll
+    for (int ks = wk; ks < L::KC / 16; ks += L::WK) {
+      uint32_t fa[4];
+      ldsm4(xs + tile_at<XC>(wm * 16 + (lane & 15), ks * 2 + (lane >> 4)), fa);
+#pragma unroll
+      for (int p = 0; p < L::NT / 2; ++p) {
+        const int j0 = wn * (RP / L::WN) + p * 16;
+        uint32_t fb[4];
+        if (!BWD)
+          ldsm4_t(ws + tile_at<RP / 8>(ks * 16 + (lane & 15), j0 / 8 + (lane >> 4)), fb);
+        else
+          ldsm4(ws + tile_at<XC>(j0 + (lane & 7) + (lane >> 4) * 8, ks * 2 + ((lane >> 3) & 1)),
+                fb);
+        mma16816(c[2 * p], fa, fb[0], fb[1]);
+        mma16816(c[2 * p + 1], fa, fb[2], fb[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] += c[i][j];
+  }
+  cp_wait<0>();
+  __syncthreads();   // the first ring is free
+
+  // ---- u (v): the warps' and then the CTAs' partial sums, in order ----
+  if (!L::AHEAD && L::WK == 1) begin2();
   {
     const int row = wm * 16 + (lane >> 2), col0 = wn * (RP / L::WN) + (lane & 3) * 2;
     float* dst = L::WK > 1 ? reinterpret_cast<float*>(smem) + wk * TM * RP : partp;
 #pragma unroll
     for (int i = 0; i < L::NT; ++i) {
       float* p = dst + row * RP + col0 + i * 8;
-      p[0] = acc[i][0];
-      p[1] = acc[i][1];
-      p[8 * RP] = acc[i][2];
-      p[8 * RP + 1] = acc[i][3];
+      *reinterpret_cast<float2*>(p) = make_float2(acc[i][0], acc[i][1]);
+      *reinterpret_cast<float2*>(p + 8 * RP) = make_float2(acc[i][2], acc[i][3]);
     }
   }
   if (L::WK > 1) {
     __syncthreads();
-    for (int i = tid; i < TM * RP; i += 256) {
-      float v = 0.f;
+    for (int i = tid * 4; i < TM * RP; i += 1024) {
+      float4 v = *reinterpret_cast<const float4*>(smem + i * 4);
 #pragma unroll
-      for (int w = 0; w < L::WK; ++w) v += reinterpret_cast<float*>(smem)[w * TM * RP + i];
-      partp[i] = v;
+      for (int w = 1; w < L::WK; ++w) {
+        const float4 q = *reinterpret_cast<const float4*>(smem + (w * TM * RP + i) * 4);
+        v.x += q.x;
+        v.y += q.y;
+        v.z += q.z;
+        v.w += q.w;
+      }
+      *reinterpret_cast<float4*>(partp + i) = v;
     }
     __syncthreads();
+    if (!L::AHEAD) begin2();
   }
-  begin2();
   if (CS > 1) cluster_sync_all();
   else __syncthreads();
-  const float sc = __ldg(scale + a);
-  for (int i = tid * 4; i < TM * RP; i += 1024) {
+  // Each CTA adds its share of the rows over the cluster and hands the bf16
+  // terms to every CTA's operand tile.
+  const float sc = __ldg(g.scale + a);
+  const int e0 = TM * cr / CS * RP, e1 = TM * (cr + 1) / CS * RP;
+  for (int i = e0 + tid * 4; i < e1; i += 1024) {
     const int row = i / RP, j = i % RP;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int q = 0; q < CS; ++q) {
@@ -408,32 +445,44 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) v[m] *= sc;
-    const int t = s_rows[row];
-    if (u != nullptr && cr == 0 && t >= 0 && j < r)
-      *reinterpret_cast<float4*>(u + (size_t)t * r + j) = make_float4(v[0], v[1], v[2], v[3]);
-    __nv_bfloat16 tm[4][L::TERMS];
+    uint2 tm[L::TERMS];
+    split4<L::TERMS>(v, tm);
+    const uint32_t at = L::RING + tile_at<RP / 8>(row, j / 8) + (j % 8) * 2;
+    for (int q = 0; q < CS; ++q) {
+      const uint32_t dst = CS > 1 ? cluster_smem_addr(smem + at, (uint32_t)q) : ring + at;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) split_bf16<L::TERMS>(v[m], tm[m]);
+      for (int w = 0; w < L::TERMS; ++w) st_cluster_v2(dst + w * TM * RP * 2, tm[w]);
+    }
+    const int t = token(row);
+    if (t < 0 || j >= r) continue;
+    if (!BWD) {
+      if (g.u != nullptr)
+        *reinterpret_cast<float4*>(g.u + (size_t)t * r + j) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      // the gradient's operands: v's and u's terms
+      const float4 uq = __ldg(reinterpret_cast<const float4*>(g.u + (size_t)t * r + j));
+      const float uv[4] = {uq.x, uq.y, uq.z, uq.w};
+      uint2 ut[3];
+      split4<3>(uv, ut);
 #pragma unroll
-    for (int w = 0; w < L::TERMS; ++w) {
-      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(
-          smem + L::RING + w * TM * RP * 2 + tile_at<RP / 8>(row, j / 8) + (j % 8) * 2);
-#pragma unroll
-      for (int m = 0; m < 4; ++m) p[m] = tm[m][w];
+      for (int w = 0; w < 3; ++w) {
+        const size_t o = ((size_t)t * 3 + w) * r + j;
+        *reinterpret_cast<uint2*>(g.vp + o) = tm[w < L::TERMS ? w : 0];
+        *reinterpret_cast<uint2*>(g.up + o) = ut[w];
+      }
     }
   }
-  if (CS > 1) cluster_sync_all();   // peers have read this CTA's partial sums
+  if (CS > 1) cluster_sync_all();
   else __syncthreads();
 
   // ---- second product: out[rows, slice] = base + u W2[:, slice] ----
   const int w2n = warp / L::WM;
-  constexpr int BC = L::NC * L::OB / 16;
   for (int nc = n0; nc < n1; ++nc) {
     cp_wait<L::ST2 - 2>();
     __syncthreads();
     if (nc + L::ST2 - 1 < n1) load2(nc + L::ST2 - 1);
     cp_commit();
-    const uint32_t so = (uint32_t)((nc - n0) % L::ST2) * L::S2;
+    const uint32_t so = L::RING2 + (uint32_t)((nc - n0) % L::ST2) * L::S2;
     const uint32_t ws = ring + so;
     float c[L::NT2][4];
 #pragma unroll
@@ -484,15 +533,14 @@ __global__ void __launch_bounds__(256)
       }
     }
     __syncthreads();
-    constexpr int PV = 16 / L::OB;
+    const int col = nc * L::NC + tid % BC * PV;
 #pragma unroll
-    for (int i = tid; i < TM * BC; i += 256) {
-      const int row = i / BC, cc = i % BC, col = nc * L::NC + cc * PV;
-      const int t = s_rows[row];
-      if (t >= 0 && col < N)
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + ((size_t)t * N + col) * L::OB) =
-            *reinterpret_cast<const uint4*>(bs + tile_at<BC>(row, cc));
-    }
+    for (int i = 0; i < BR; ++i)
+      if (bt[i] >= 0 && col < N)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.out) +
+                                  ((size_t)bt[i] * N + col) * L::OB) =
+            *reinterpret_cast<const uint4*>(bs +
+                                            tile_at<BC>(tid / BC + i * (256 / BC), tid % BC));
   }
   cp_wait<0>();
 }
@@ -501,6 +549,7 @@ __global__ void __launch_bounds__(256)
 
 constexpr int kGradCols = 128;   // columns of x (dA) or dy (dB) a CTA
 constexpr int kGradRows = 32;    // rows a stage
+constexpr int kGradMax = 2048;   // rows of a part, at most
 
 template <int RP>
 struct Grad {
@@ -508,18 +557,17 @@ struct Grad {
   static constexpr int MT = WN;                    // 16-column tiles a warp (8 / WN warps along m)
   static constexpr int NT = RP / 8 / WN;
   static constexpr int XS = kGradRows * kGradCols * 2;
-  static constexpr int VS = kGradRows * RP * 4;
-  static constexpr int STAGE = XS + VS;
+  static constexpr int VS = kGradRows * RP * 2;    // one of the three terms
+  static constexpr int STAGE = XS + 3 * VS;
   static constexpr int STAGES = 4;
-  static constexpr int TS = 3 * kGradRows * RP * 2;
-  static constexpr int SMEM = STAGES * STAGE + TS;
+  static constexpr int SMEM = STAGES * STAGE + kGradMax * 4;
 };
 
 struct GradArgs {
   const __nv_bfloat16* x;   // (T, d)
   const __nv_bfloat16* dy;  // (T, d_out)
-  const float* u;           // (T, r)
-  const float* v;           // (T, r)
+  const __nv_bfloat16* up;  // (T, 3, r): u's three terms
+  const __nv_bfloat16* vp;  // (T, 3, r): v's
   float* dA;                // (n, d, r)
   float* dB;                // (n, r, d_out)
   float* part;              // (slots, r (d + d_out)): parts of split adapters, dA's then dB's
@@ -527,15 +575,16 @@ struct GradArgs {
   const int32_t* offsets;
   const int32_t* rows;
   int32_t* err;
-  int T, n, r, d, d_out, len;   // len: rows between split positions
+  int T, n, r, d, d_out, len;   // len: rows of a part, at most
 };
 
-// The adapter whose part has slot `slot` = (row block) + (adapter): the last
-// a with offsets[a] / len + a <= slot.
+// An adapter of c rows has ceil(c / len) parts of equal length; part i of
+// adapter a has the slot offsets[a] / len + a + i, which no other part has.
+// The adapter of a slot: the last a with offsets[a] / len + a <= slot.
 __device__ __forceinline__ int find_adapter(const int32_t* __restrict__ offsets, int n, int len,
                                             int slot) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;   // the answer + 1 is in (lo, hi]: adapter 0 always satisfies it
+  int lo = 0, hi = n;   // the answer + 1 is in [lo, hi]
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
@@ -549,11 +598,12 @@ __device__ __forceinline__ int find_adapter(const int32_t* __restrict__ offsets,
 }
 
 template <int RP>
-__global__ void __launch_bounds__(256) adapter_grad_kernel(GradArgs g) {
+__global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) adapter_grad_kernel(GradArgs g) {
   using L = Grad<RP>;
   pdl_wait_and_release();
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t ring = smem_u32(smem), ts = ring + L::STAGES * L::STAGE;
+  const uint32_t ring = smem_u32(smem);
+  int32_t* s_rows = reinterpret_cast<int32_t*>(smem + L::STAGES * L::STAGE);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (__ldg(g.header) != g.T || __ldg(g.header + 1) != g.n) {
     if (tid == 0) report_error(g.err, kDevBadPlan);
@@ -562,33 +612,37 @@ __global__ void __launch_bounds__(256) adapter_grad_kernel(GradArgs g) {
   const int slot = blockIdx.y;
   const int a = find_adapter(g.offsets, g.n, g.len, slot);
   if (a < 0) return;
-  const int o0 = __ldg(g.offsets + a), o1 = __ldg(g.offsets + a + 1);
-  const long long blk = slot - a;
-  const int r0 = (int)max((long long)o0, blk * g.len);
-  const int r1 = (int)min((long long)o1, (blk + 1) * g.len);
-  if (r0 >= r1) return;
-  const bool whole = r0 == o0 && r1 == o1;   // the adapter's only part: straight to the gradient
+  const int o0 = __ldg(g.offsets + a), cnt = __ldg(g.offsets + a + 1) - o0;
+  const int parts = ceil_div_dev(cnt, g.len), pi = slot - (o0 / g.len + a);
+  if (pi >= parts) return;
+  const int r0 = o0 + (int)((long long)cnt * pi / parts);
+  const int nr = o0 + (int)((long long)cnt * (pi + 1) / parts) - r0;   // <= len
   const int mbx = ceil_div_dev(g.d, kGradCols);
   const bool isA = (int)blockIdx.x < mbx;
   const int m0 = (isA ? blockIdx.x : blockIdx.x - mbx) * kGradCols;
   const int M = isA ? g.d : g.d_out, r = g.r;
   const __nv_bfloat16* X = isA ? g.x : g.dy;
-  const float* V = isA ? g.v : g.u;
-  const int nst = ceil_div_dev(r1 - r0, kGradRows);
+  const __nv_bfloat16* V = isA ? g.vp : g.up;
+  for (int i = tid; i < nr; i += 256) s_rows[i] = __ldg(g.rows + r0 + i);
+  __syncthreads();
+  const int nst = ceil_div_dev(nr, kGradRows);
   auto load = [&](int s) {
-    const uint32_t xs = ring + (uint32_t)(s % L::STAGES) * L::STAGE, vs = xs + L::XS;
-    constexpr int XC = kGradCols / 8, VC = RP / 4;
+    const uint32_t xs = ring + (uint32_t)(s % L::STAGES) * L::STAGE;
+    constexpr int XC = kGradCols / 8, VC = RP / 8;
 #pragma unroll
     for (int i = tid; i < kGradRows * XC; i += 256) {
-      const int row = i / XC, c = i % XC, col = m0 + c * 8, at = r0 + s * kGradRows + row;
-      const bool ok = at < r1 && col < M;
-      cp_async16(xs + tile_at<XC>(row, c), ok ? X + (size_t)__ldg(g.rows + at) * M + col : X, ok);
+      const int row = i / XC, c = i % XC, col = m0 + c * 8, at = s * kGradRows + row;
+      const bool ok = at < nr && col < M;
+      cp_async16(xs + tile_at<XC>(row, c), ok ? X + (size_t)s_rows[at] * M + col : X, ok);
     }
 #pragma unroll
     for (int i = tid; i < kGradRows * VC; i += 256) {
-      const int row = i / VC, c = i % VC, at = r0 + s * kGradRows + row;
-      const bool ok = at < r1 && c * 4 < r;
-      cp_async16(vs + i * 16, ok ? V + (size_t)__ldg(g.rows + at) * r + c * 4 : V, ok);
+      const int row = i / VC, c = i % VC, at = s * kGradRows + row;
+      const bool ok = at < nr && c * 8 < r;
+      const __nv_bfloat16* src = ok ? V + (size_t)s_rows[at] * 3 * r + c * 8 : V;
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+        cp_async16(xs + L::XS + w * L::VS + tile_at<VC>(row, c), ok ? src + w * r : V, ok);
     }
   };
   const int wm = warp / L::WN, wn = warp % L::WN;
@@ -609,26 +663,7 @@ __global__ void __launch_bounds__(256) adapter_grad_kernel(GradArgs g) {
     __syncthreads();
     if (s + L::STAGES - 1 < nst) load(s + L::STAGES - 1);
     cp_commit();
-    const uint32_t so = (uint32_t)(s % L::STAGES) * L::STAGE;
-    // the stage's v (or u) as three bf16 terms
-#pragma unroll
-    for (int i = tid; i < kGradRows * RP / 4; i += 256) {
-      const int row = i / (RP / 4), j = i % (RP / 4) * 4;
-      const float4 q = *reinterpret_cast<const float4*>(smem + so + L::XS + i * 16);
-      const float v[4] = {q.x, q.y, q.z, q.w};
-      __nv_bfloat16 t[4][3];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) split_bf16<3>(v[m], t[m]);
-#pragma unroll
-      for (int w = 0; w < 3; ++w) {
-        __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(
-            smem + L::STAGES * L::STAGE + w * kGradRows * RP * 2 + tile_at<RP / 8>(row, j / 8) +
-            (j % 8) * 2);
-        p[0] = __nv_bfloat162(t[0][w], t[1][w]);
-        p[1] = __nv_bfloat162(t[2][w], t[3][w]);
-      }
-    }
-    __syncthreads();
+    const uint32_t xs = ring + (uint32_t)(s % L::STAGES) * L::STAGE, vs = xs + L::XS;
     float c[L::MT][L::NT][4];
 #pragma unroll
     for (int m = 0; m < L::MT; ++m)
@@ -641,17 +676,16 @@ __global__ void __launch_bounds__(256) adapter_grad_kernel(GradArgs g) {
       uint32_t fa[L::MT][4];
 #pragma unroll
       for (int m = 0; m < L::MT; ++m)
-        ldsm4_t(ring + so + tile_at<kGradCols / 8>(ks * 16 + (lane & 7) + (lane >> 4) * 8,
-                                                   (wm * L::MT + m) * 2 + ((lane >> 3) & 1)),
-                fa[m]);
+        ldsm4_t(xs + tile_at<kGradCols / 8>(ks * 16 + (lane & 7) + (lane >> 4) * 8,
+                                            (wm * L::MT + m) * 2 + ((lane >> 3) & 1)), fa[m]);
 #pragma unroll
       for (int w = 2; w >= 0; --w) {
 #pragma unroll
         for (int p = 0; p < L::NT / 2; ++p) {
           const int j0 = wn * (RP / L::WN) + p * 16;
           uint32_t fb[4];
-          ldsm4_t(ts + w * kGradRows * RP * 2 +
-                      tile_at<RP / 8>(ks * 16 + (lane & 15), j0 / 8 + (lane >> 4)), fb);
+          ldsm4_t(vs + w * L::VS + tile_at<RP / 8>(ks * 16 + (lane & 15), j0 / 8 + (lane >> 4)),
+                  fb);
 #pragma unroll
           for (int m = 0; m < L::MT; ++m) {
             mma16816(c[m][2 * p], fa[m], fb[0], fb[1]);
@@ -669,8 +703,9 @@ __global__ void __launch_bounds__(256) adapter_grad_kernel(GradArgs g) {
   }
   cp_wait<0>();
   const size_t dsz = (size_t)g.d * r, bsz = (size_t)g.d_out * r;
-  float* out = whole ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
-                     : g.part + (size_t)slot * (dsz + bsz) + (isA ? 0 : dsz);
+  // the adapter's only part goes straight to the gradient
+  float* out = parts == 1 ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
+                          : g.part + (size_t)slot * (dsz + bsz) + (isA ? 0 : dsz);
 #pragma unroll
   for (int m = 0; m < L::MT; ++m)
 #pragma unroll
@@ -696,15 +731,17 @@ __global__ void __launch_bounds__(256) adapter_reduce_kernel(GradArgs g) {
   pdl_wait_and_release();
   if (__ldg(g.header) != g.T || __ldg(g.header + 1) != g.n) return;
   const int a = blockIdx.y;
-  const int o0 = __ldg(g.offsets + a), o1 = __ldg(g.offsets + a + 1);
-  const int b0 = o0 / g.len, b1 = o1 > o0 ? (o1 - 1) / g.len : b0 - 1;   // first and last block
-  if (b0 == b1) return;
+  const int o0 = __ldg(g.offsets + a), cnt = __ldg(g.offsets + a + 1) - o0;
+  const int parts = ceil_div_dev(cnt, g.len);
+  if (parts == 1) return;
   const size_t dsz = (size_t)g.d * g.r, bsz = (size_t)g.d_out * g.r, all = dsz + bsz;
+  const float* src = g.part + (size_t)(o0 / g.len + a) * all;
   for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all;
        i += (size_t)gridDim.x * 1024) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = b0; b <= b1; ++b) {
-      const float4 p = *reinterpret_cast<const float4*>(g.part + (size_t)(b + a) * all + i);
+#pragma unroll 4
+    for (int b = 0; b < parts; ++b) {
+      const float4 p = *reinterpret_cast<const float4*>(src + (size_t)b * all + i);
       s.x += p.x;
       s.y += p.y;
       s.z += p.z;
@@ -723,12 +760,12 @@ int tile_rows(int T, int n) { return T <= 1024 || T <= 32 * n ? 16 : 64; }
 
 int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
 
-// Rows between the positions at which the gradient's contraction is split:
-// about four CTAs an SM, at least 256 rows.
+// Rows of a part of the gradient's contraction, at most: one part for each CTA
+// that the SMs hold at a time (two an SM) were the adapters even.
 int grad_len(const moe_config_t& c) {
-  const int mb = ceil_div(c.d, kGradCols) + ceil_div(c.d_out, kGradCols);
-  const int parts = std::max(1, ceil_div(4 * 148, mb));
-  return std::max(256, ceil_div(ceil_div(c.T, parts), kGradRows) * kGradRows);
+  const int64_t mb = ceil_div(c.d, kGradCols) + ceil_div(c.d_out, kGradCols);
+  const int64_t rows = (c.T * mb + 2 * 148 - 1) / (2 * 148);
+  return (int)std::min<int64_t>(kGradMax, std::max<int64_t>(256, (rows + 31) / 32 * 32));
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -750,8 +787,9 @@ AdapterWsLayout adapter_ws_layout(const moe_config_t& c, int n, int r) {
   AdapterWsLayout L{};
   const int len = grad_len(c);
   L.v = 0;
-  L.part = up256((size_t)c.T * r * 4);
-  // an adapter needs parts only if its rows cross a split position
+  L.u = up256((size_t)c.T * r * 6);
+  L.part = 2 * L.u;
+  // an adapter has several parts only if it has more rows than one takes
   const size_t slots = c.T > len ? (size_t)(c.T / len + n + 1) : 0;
   L.total = L.part + up256(slots * (size_t)r * ((size_t)c.d + c.d_out) * 4) + 256;
   return L;
@@ -775,19 +813,21 @@ cudaError_t run_low_rank(const AdapterCall& a, cudaStream_t s) {
   using L = LowRank<RP, TM, BWD>;
   const AdapterPlanLayout P = adapter_plan_layout(*a.c, a.n);
   uint8_t* p = static_cast<uint8_t*>(a.plan);
-  // CTAs of a tile's cluster: enough to give every SM about four
+  // CTAs of a tile's cluster: as many as the SMs hold at a time
   const int tiles = max_tiles(a.c->T, a.n);
   const int most = std::min(ceil_div(a.K, L::KC), ceil_div(a.N, L::NC));
+  const int64_t room = (int64_t)std::min(L::CTAS, 4) * device_sm_count();
   int cs = 1;
-  while (cs < 8 && cs * 2 <= most && tiles * cs < 4 * device_sm_count()) cs *= 2;
+  while (cs < 8 && cs * 2 <= most && (int64_t)tiles * cs * 2 <= room) cs *= 2;
   const auto kern = low_rank_kernel<RP, TM, BWD>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, (unsigned)tiles * cs, 256, L::SMEM, s, cs, a.in, a.W1, a.W2, a.scale,
-                       a.base, a.out, a.u, a.c->T, a.n, a.r, a.K, a.N,
-                       reinterpret_cast<const int32_t*>(p + P.header),
-                       reinterpret_cast<const int32_t*>(p + P.rows),
-                       reinterpret_cast<const int4*>(p + P.tiles), reinterpret_cast<int32_t*>(p));
+  const LowRankArgs g{a.in, a.W1, a.W2, a.scale, a.base, a.out, a.u, a.up, a.vp,
+                      reinterpret_cast<const int32_t*>(p + P.header),
+                      reinterpret_cast<const int32_t*>(p + P.rows),
+                      reinterpret_cast<const int4*>(p + P.tiles), reinterpret_cast<int32_t*>(p),
+                      a.c->T, a.n, a.r, a.K, a.N};
+  return launch_kernel(kern, (unsigned)tiles * cs, 256, L::SMEM, s, cs, g);
 }
 
 template <int RP, bool BWD>
@@ -824,8 +864,7 @@ cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s) 
 }
 
 cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan, const void* x,
-                                const float* u, const void* dy, float* dA, float* dB, void* ws,
-                                cudaStream_t s) {
+                                const void* dy, float* dA, float* dB, void* ws, cudaStream_t s) {
   const size_t dsz = (size_t)c.d * r * n * 4, bsz = (size_t)c.d_out * r * n * 4;
   if (c.T == 0) {
     cudaError_t e = cudaMemsetAsync(dA, 0, dsz, s);
@@ -835,8 +874,9 @@ cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan,
   const AdapterWsLayout W = adapter_ws_layout(c, n, r);
   uint8_t* p = static_cast<uint8_t*>(plan);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const GradArgs g{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(dy), u,
-                   reinterpret_cast<const float*>(w + W.v), dA, dB,
+  const GradArgs g{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(dy),
+                   reinterpret_cast<const __nv_bfloat16*>(w + W.u),
+                   reinterpret_cast<const __nv_bfloat16*>(w + W.v), dA, dB,
                    reinterpret_cast<float*>(w + W.part),
                    reinterpret_cast<const int32_t*>(p + P.header),
                    reinterpret_cast<const int32_t*>(p + P.offsets),

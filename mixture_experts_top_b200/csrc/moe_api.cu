@@ -822,7 +822,8 @@ int moe_adapter(const moe_config_t* cfg, int32_t n_adapters, int32_t rank, void*
     return st;
   const AdapterCall a{&c, n_adapters, rank, c.d, c.d_out, plan,
                       static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(A),
-                      static_cast<const __nv_bfloat16*>(B), scale, base, output, u};
+                      static_cast<const __nv_bfloat16*>(B), scale, base, output, u, nullptr,
+                      nullptr};
   const cudaError_t e = launch_adapter(a, false, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_adapter");
 }
@@ -864,10 +865,11 @@ int moe_adapter_backward(const moe_config_t* cfg, int32_t n_adapters, int32_t ra
   const AdapterCall a{&c, n_adapters, rank, c.d_out, c.d, plan,
                       static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(B),
                       static_cast<const __nv_bfloat16*>(A), scale, dx_add, dx,
-                      at<float>(ws, W.v)};
+                      const_cast<float*>(u), at<__nv_bfloat16>(ws, W.u),
+                      at<__nv_bfloat16>(ws, W.v)};
   cudaError_t e = launch_adapter(a, true, s);
   if (e == cudaSuccess)
-    e = launch_adapter_grad(c, n_adapters, rank, plan, x, u, dy, dA, dB, ws, s);
+    e = launch_adapter_grad(c, n_adapters, rank, plan, x, dy, dA, dB, ws, s);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_adapter_backward");
 }
 

@@ -313,16 +313,17 @@ struct AdapterPlanLayout {
   size_t total;
 };
 AdapterPlanLayout adapter_plan_layout(const moe_config_t& c, int n);
-// v (T, r) fp32 and the parts of split adapters' gradients.
+// v's and u's three bf16 terms (T, 3, r), and the parts of split adapters'
+// gradients.
 struct AdapterWsLayout {
-  size_t v, part, total;
+  size_t v, u, part, total;
 };
 AdapterWsLayout adapter_ws_layout(const moe_config_t& c, int n, int r);
 cudaError_t launch_adapter_plan(const moe_config_t& c, int n, const int32_t* ids, void* plan,
                                 cudaStream_t s);
 // Two products of every row tile: forward in = x, K = d, N = d_out, out and
-// base bf16; backward in = dy, K = d_out, N = d, out and base fp32, W1 = B,
-// W2 = A, u = v.
+// base bf16, u out or null; backward in = dy, K = d_out, N = d, out and base
+// fp32, W1 = B, W2 = A, u the forward's, up and vp the workspace's terms.
 struct AdapterCall {
   const moe_config_t* c;
   int n, r, K, N;
@@ -332,11 +333,11 @@ struct AdapterCall {
   const void* base;
   void* out;
   float* u;
+  __nv_bfloat16 *up, *vp;
 };
 cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s);
 cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan, const void* x,
-                                const float* u, const void* dy, float* dA, float* dB, void* ws,
-                                cudaStream_t s);
+                                const void* dy, float* dA, float* dB, void* ws, cudaStream_t s);
 
 // One bounded mbarrier wait that nothing completes; after limit_ns the kernel
 // writes the self-test code to err and returns (moe_api.cu).
