@@ -25,79 +25,12 @@
 // at a time and the blocks are added in round-to-nearest fp32.  u and v are
 // fp32 values: where one is an operand it is split into bf16 terms, two
 // (16 bits) for the bf16 output, three (all 24 bits) for the fp32 gradients.
+#include "adapter.cuh"
 #include "moe_device.cuh"
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
-
-// ---------------------------------------------------------------- helpers --
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;   // 0: the 16 bytes are filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-// Byte offset of 16-byte piece c of row `row` in a tile of CPR pieces a row
-// (a power of two): the 8 rows a matrix load reads fall on distinct banks.
-template <int CPR>
-__device__ __forceinline__ uint32_t tile_at(int row, int c) {
-  constexpr int kPer = CPR >= 8 ? 1 : 8 / CPR;   // rows in 128 bytes
-  const int sw = (row / kPer) & (CPR >= 8 ? 7 : CPR - 1);
-  return (uint32_t)(row * CPR + (c ^ sw)) * 16u;
-}
-
-// Four values as a sum of N bf16 terms each: t[i] holds the four i-th terms.
-template <int N>
-__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&t)[N]) {
-  float a = v[0], b = v[1], c = v[2], d = v[3];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    t[i] = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
-    a -= __uint_as_float(t[i].x << 16);
-    b -= __uint_as_float(t[i].x & 0xFFFF0000u);
-    c -= __uint_as_float(t[i].y << 16);
-    d -= __uint_as_float(t[i].y & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint2 v) {
-  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y)
-               : "memory");
-}
 
 // ------------------------------------------------------------------- plan --
 
@@ -195,23 +128,6 @@ struct LowRank {
   static constexpr int PART = TM * RP * 4;
   static constexpr int SMEM = RING + US + PART;
   static constexpr int CTAS = 227 * 1024 / (SMEM + 1024 + TM * 4);   // an SM holds, by memory
-};
-
-struct LowRankArgs {
-  const __nv_bfloat16* in;    // (T, K)
-  const __nv_bfloat16* W1;    // per adapter: forward A (K, r), backward B (r, K)
-  const __nv_bfloat16* W2;    // per adapter: forward B (r, N), backward A (N, r)
-  const float* scale;
-  const void* base;           // (T, N), bf16 forward, fp32 backward; null (0) or out
-  void* out;                  // (T, N)
-  float* u;                   // forward: (T, r) out or null; backward: the forward's
-  __nv_bfloat16* up;          // backward: u's and v's three terms out, (T, 3, r)
-  __nv_bfloat16* vp;
-  const int32_t* header;
-  const int32_t* rows;
-  const int4* tiles;
-  int32_t* err;
-  int T, n, r, K, N;
 };
 
 template <int RP, int TM, bool BWD>
@@ -547,21 +463,33 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
 
 // --------------------------------------------------------------- gradient --
 
-constexpr int kGradCols = 128;   // columns of x (dA) or dy (dB) a CTA
+// On tcgen05: D (128 columns of x or dy, 3 r) = X^T [v0 | v1 | v2], the three
+// terms side by side on the MMA's N, so that X is read from shared memory once
+// for all of them; the epilogue adds a row's three column groups.  Both
+// operands run down their rows on the contraction (MN-major, 128-byte swizzle:
+// boxes of 64 columns x 32 rows).  Warps 0-3 gather rows into the stages by
+// cp.async, then read tensor memory; warp 4 issues the MMAs.
+constexpr int kGradCols = 128;   // columns of x (dA) or dy (dB) a CTA: the MMA's M
 constexpr int kGradRows = 32;    // rows a stage
-constexpr int kGradMax = 2048;   // rows of a part, at most
+// Rows of a part, at most: the tensor core's fp32 sums of 1024 rows keep the
+// gradients within 8e-7 of exact, normwise; the parts are added in
+// round-to-nearest fp32.
+constexpr int kGradMax = 1024;
+constexpr int kGradBox = kGradRows * 128;           // 64 bf16 columns of a stage's rows
+constexpr int kGradThreads = 160;
+constexpr int kGradAux = 1024 + kGradMax * 4;       // barriers, tmem address, rows
 
-template <int RP>
-struct Grad {
-  static constexpr int WN = RP >= 32 ? 2 : 1;
-  static constexpr int MT = WN;                    // 16-column tiles a warp (8 / WN warps along m)
-  static constexpr int NT = RP / 8 / WN;
-  static constexpr int XS = kGradRows * kGradCols * 2;
-  static constexpr int VS = kGradRows * RP * 2;    // one of the three terms
-  static constexpr int STAGE = XS + 3 * VS;
-  static constexpr int STAGES = 4;
-  static constexpr int SMEM = STAGES * STAGE + kGradMax * 4;
-};
+// The MN-major descriptor: boxes along MN kGradBox apart, 8-row groups 1024
+// bytes apart, 128-byte swizzle; a k step of 16 rows is 2048 bytes.
+__device__ __forceinline__ uint64_t grad_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(kGradBox >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// D fp32, A and B bf16, both MN-major, M = 128; N >> 3 at bit 17.
+__device__ __forceinline__ uint32_t grad_idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+         ((uint32_t)(kGradCols >> 4) << 24) | ((uint32_t)(n >> 3) << 17);
+}
 
 struct GradArgs {
   const __nv_bfloat16* x;   // (T, d)
@@ -576,6 +504,7 @@ struct GradArgs {
   const int32_t* rows;
   int32_t* err;
   int T, n, r, d, d_out, len;   // len: rows of a part, at most
+  int N, stage_bytes, tmem_cols;   // 3 r rounded up to 16; x's boxes and the terms'
 };
 
 // An adapter of c rows has ceil(c / len) parts of equal length; part i of
@@ -597,13 +526,17 @@ __device__ __forceinline__ int find_adapter(const int32_t* __restrict__ offsets,
   return lo - 1;
 }
 
-template <int RP>
-__global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) adapter_grad_kernel(GradArgs g) {
-  using L = Grad<RP>;
+template <int STAGES>
+__global__ void __launch_bounds__(kGradThreads, 2) adapter_grad_kernel(GradArgs g) {
   pdl_wait_and_release();
-  extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t ring = smem_u32(smem);
-  int32_t* s_rows = reinterpret_cast<int32_t*>(smem + L::STAGES * L::STAGE);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + STAGES * g.stage_bytes);
+  uint64_t* empty_bar = full_bar + STAGES;
+  uint64_t* done_bar = empty_bar + STAGES;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
+  int32_t* s_rows = reinterpret_cast<int32_t*>(smem + STAGES * g.stage_bytes + 256);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (__ldg(g.header) != g.T || __ldg(g.header + 1) != g.n) {
     if (tid == 0) report_error(g.err, kDevBadPlan);
@@ -616,114 +549,123 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) adapter_grad_kernel(Gra
   const int parts = ceil_div_dev(cnt, g.len), pi = slot - (o0 / g.len + a);
   if (pi >= parts) return;
   const int r0 = o0 + (int)((long long)cnt * pi / parts);
-  const int nr = o0 + (int)((long long)cnt * (pi + 1) / parts) - r0;   // <= len
+  const int nr = o0 + (int)((long long)cnt * (pi + 1) / parts) - r0;   // 1 .. len
   const int mbx = ceil_div_dev(g.d, kGradCols);
   const bool isA = (int)blockIdx.x < mbx;
   const int m0 = (isA ? blockIdx.x : blockIdx.x - mbx) * kGradCols;
-  const int M = isA ? g.d : g.d_out, r = g.r;
+  const int M = isA ? g.d : g.d_out, r = g.r, r3 = 3 * g.r;
   const __nv_bfloat16* X = isA ? g.x : g.dy;
   const __nv_bfloat16* V = isA ? g.vp : g.up;
-  for (int i = tid; i < nr; i += 256) s_rows[i] = __ldg(g.rows + r0 + i);
+  for (int i = tid; i < nr; i += kGradThreads) s_rows[i] = __ldg(g.rows + r0 + i);
+  if (warp == 4) {
+    tmem_alloc(tmem_holder, (uint32_t)g.tmem_cols);
+    tmem_relinquish();
+    if (lane == 0) {
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(&full_bar[s], 128);  // each producer's copies
+        mbar_init(&empty_bar[s], 1);   // the MMAs that read the stage
+      }
+      mbar_init(done_bar, 1);
+      fence_mbar_init();
+    }
+  }
+  tc_fence_before_sync();
   __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
   const int nst = ceil_div_dev(nr, kGradRows);
-  auto load = [&](int s) {
-    const uint32_t xs = ring + (uint32_t)(s % L::STAGES) * L::STAGE;
-    constexpr int XC = kGradCols / 8, VC = RP / 8;
-#pragma unroll
-    for (int i = tid; i < kGradRows * XC; i += 256) {
-      const int row = i / XC, c = i % XC, col = m0 + c * 8, at = s * kGradRows + row;
-      const bool ok = at < nr && col < M;
-      cp_async16(xs + tile_at<XC>(row, c), ok ? X + (size_t)s_rows[at] * M + col : X, ok);
-    }
-#pragma unroll
-    for (int i = tid; i < kGradRows * VC; i += 256) {
-      const int row = i / VC, c = i % VC, at = s * kGradRows + row;
-      const bool ok = at < nr && c * 8 < r;
-      const __nv_bfloat16* src = ok ? V + (size_t)s_rows[at] * 3 * r + c * 8 : V;
-#pragma unroll
-      for (int w = 0; w < 3; ++w)
-        cp_async16(xs + L::XS + w * L::VS + tile_at<VC>(row, c), ok ? src + w * r : V, ok);
-    }
-  };
-  const int wm = warp / L::WN, wn = warp % L::WN;
-  float acc[L::MT][L::NT][4];
-#pragma unroll
-  for (int m = 0; m < L::MT; ++m)
-#pragma unroll
-    for (int i = 0; i < L::NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.f;
-#pragma unroll
-  for (int i = 0; i < L::STAGES - 1; ++i) {
-    if (i < nst) load(i);
-    cp_commit();
-  }
-  for (int s = 0; s < nst; ++s) {
-    cp_wait<L::STAGES - 2>();
-    __syncthreads();
-    if (s + L::STAGES - 1 < nst) load(s + L::STAGES - 1);
-    cp_commit();
-    const uint32_t xs = ring + (uint32_t)(s % L::STAGES) * L::STAGE, vs = xs + L::XS;
-    float c[L::MT][L::NT][4];
-#pragma unroll
-    for (int m = 0; m < L::MT; ++m)
-#pragma unroll
-      for (int i = 0; i < L::NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[m][i][j] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < kGradRows / 16; ++ks) {
-      uint32_t fa[L::MT][4];
-#pragma unroll
-      for (int m = 0; m < L::MT; ++m)
-        ldsm4_t(xs + tile_at<kGradCols / 8>(ks * 16 + (lane & 7) + (lane >> 4) * 8,
-                                            (wm * L::MT + m) * 2 + ((lane >> 3) & 1)), fa[m]);
-#pragma unroll
-      for (int w = 2; w >= 0; --w) {
-#pragma unroll
-        for (int p = 0; p < L::NT / 2; ++p) {
-          const int j0 = wn * (RP / L::WN) + p * 16;
-          uint32_t fb[4];
-          ldsm4_t(vs + w * L::VS + tile_at<RP / 8>(ks * 16 + (lane & 15), j0 / 8 + (lane >> 4)),
-                  fb);
-#pragma unroll
-          for (int m = 0; m < L::MT; ++m) {
-            mma16816(c[m][2 * p], fa[m], fb[0], fb[1]);
-            mma16816(c[m][2 * p + 1], fa[m], fb[2], fb[3]);
-          }
+
+  if (warp < 4) {
+    // ---- producers
+    const int nc = g.N / 8;
+    const int vrow = tid / 4;
+    bool alive = true;
+    for (int s = 0; s < nst; ++s) {
+      if (s >= STAGES) {
+        alive = mbar_wait(&empty_bar[s % STAGES], (uint32_t)(s / STAGES - 1) & 1u);
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) {
+          report_error(g.err, kDevTimeoutProducer);
+          break;
         }
       }
+      const uint32_t xs = smem_u32(smem + (s % STAGES) * g.stage_bytes), vs = xs + 2 * kGradBox;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = tid / 16 + 8 * i, c = tid % 16, col = m0 + c * 8, at = s * kGradRows + row;
+        const bool ok = at < nr && col < M;
+        cp_async16(xs + (c / 8) * kGradBox + tile_at<8>(row, c % 8),
+                   ok ? X + (size_t)s_rows[at] * M + col : X, ok);
+      }
+      const int at = s * kGradRows + vrow;
+      const __nv_bfloat16* src = at < nr ? V + (size_t)s_rows[at] * r3 : V;
+      for (int c = tid % 4; c < nc; c += 4) {
+        const bool ok = at < nr && c * 8 < r3;
+        cp_async16(vs + (c / 8) * kGradBox + tile_at<8>(vrow, c % 8), ok ? src + c * 8 : V, ok);
+      }
+      cp_arrive(&full_bar[s % STAGES]);
     }
+    cp_wait_all();
+    // ---- epilogue: lane = column of x, tensor-memory columns = the three terms
+    const bool ready = __all_sync(0xffffffffu, alive && mbar_wait(done_bar, 0));
+    if (alive && !ready) report_error(g.err, kDevTimeoutEpilogue);
+    tc_fence_after_sync();
+    const size_t dsz = (size_t)g.d * r, bsz = (size_t)g.d_out * r;
+    // the adapter's only part goes straight to the gradient
+    float* out = parts == 1 ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
+                            : g.part + (size_t)slot * (dsz + bsz) + (isA ? 0 : dsz);
+    const int m = m0 + warp * 32 + lane;
+    const uint32_t acc = tmem + ((uint32_t)(warp * 32) << 16);
+    for (int j = 0; ready && j < r; j += 8) {
+      uint32_t t0[8], t1[8], t2[8];
+      tmem_ld_32x32b_x8(acc + (uint32_t)j, t0);
+      tmem_ld_32x32b_x8(acc + (uint32_t)(r + j), t1);
+      tmem_ld_32x32b_x8(acc + (uint32_t)(2 * r + j), t2);
+      tmem_ld_wait();
+      float v[8];
 #pragma unroll
-    for (int m = 0; m < L::MT; ++m)
+      for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float(t0[i]) + (__uint_as_float(t1[i]) + __uint_as_float(t2[i]));
+      if (m >= M) continue;
+      if (isA) {
+        float4* o = reinterpret_cast<float4*>(out + (size_t)m * r + j);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < L::NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[m][i][j] += c[m][i][j];
-  }
-  cp_wait<0>();
-  const size_t dsz = (size_t)g.d * r, bsz = (size_t)g.d_out * r;
-  // the adapter's only part goes straight to the gradient
-  float* out = parts == 1 ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
-                          : g.part + (size_t)slot * (dsz + bsz) + (isA ? 0 : dsz);
-#pragma unroll
-  for (int m = 0; m < L::MT; ++m)
-#pragma unroll
-    for (int i = 0; i < L::NT; ++i) {
-      const int j = wn * (RP / L::WN) + i * 8 + (lane & 3) * 2;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int mm = m0 + (wm * L::MT + m) * 16 + (lane >> 2) + h * 8;
-        if (mm >= M || j >= r) continue;
-        if (isA) {
-          *reinterpret_cast<float2*>(out + (size_t)mm * r + j) =
-              make_float2(acc[m][i][2 * h], acc[m][i][2 * h + 1]);
-        } else {
-          out[(size_t)j * M + mm] = acc[m][i][2 * h];
-          out[(size_t)(j + 1) * M + mm] = acc[m][i][2 * h + 1];
-        }
+        for (int i = 0; i < 8; ++i) out[(size_t)(j + i) * M + m] = v[i];
       }
     }
+    tc_fence_before_sync();
+  } else if (lane == 0) {
+    // ---- MMA issuer
+    for (int s = 0; s < nst; ++s) {
+      if (!mbar_wait(&full_bar[s % STAGES], (uint32_t)(s / STAGES) & 1u)) {
+        report_error(g.err, kDevTimeoutMma);
+        break;
+      }
+      fence_proxy_async_smem();   // the copies' writes, before the tensor core reads them
+      tc_fence_after_sync();
+      const uint32_t xs = smem_u32(smem + (s % STAGES) * g.stage_bytes), vs = xs + 2 * kGradBox;
+#pragma unroll
+      for (int kk = 0; kk < kGradRows / 16; ++kk) {
+        const uint64_t ad = grad_desc(xs + kk * 2048);
+        const uint32_t more = (s | kk) != 0 ? 1u : 0u;
+        umma_bf16_ss(tmem, ad, grad_desc(vs + kk * 2048), grad_idesc(min(g.N, 256)), more);
+        if (g.N > 256)
+          umma_bf16_ss(tmem + 256, ad, grad_desc(vs + 4 * kGradBox + kk * 2048),
+                       grad_idesc(g.N - 256), more);
+      }
+      umma_commit(&empty_bar[s % STAGES]);
+    }
+    umma_commit(done_bar);
+    if (!mbar_wait(done_bar, 0)) report_error(g.err, kDevTimeoutDrain);
+  }
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, (uint32_t)g.tmem_cols);
+  }
 }
 
 // Adapters in parts: the parts added in order; adapters without rows: zeros.
@@ -757,6 +699,8 @@ int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 // Rows of a tile: 16 where there are few rows, in all or an adapter (decode),
 // so that they spread over the SMs and a tile is not mostly padding.
 int tile_rows(int T, int n) { return T <= 1024 || T <= 32 * n ? 16 : 64; }
+
+constexpr int kTcRows = 4096;
 
 int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
 
@@ -808,11 +752,19 @@ cudaError_t launch_adapter_plan(const moe_config_t& c, int n, const int32_t* ids
 
 namespace {
 
+LowRankArgs low_rank_args(const AdapterCall& a) {
+  const AdapterPlanLayout P = adapter_plan_layout(*a.c, a.n);
+  uint8_t* p = static_cast<uint8_t*>(a.plan);
+  return LowRankArgs{a.in, a.W1, a.W2, a.scale, a.base, a.out, a.u, a.up, a.vp,
+                     reinterpret_cast<const int32_t*>(p + P.header),
+                     reinterpret_cast<const int32_t*>(p + P.rows),
+                     reinterpret_cast<const int4*>(p + P.tiles), reinterpret_cast<int32_t*>(p),
+                     a.c->T, a.n, a.r, a.K, a.N};
+}
+
 template <int RP, int TM, bool BWD>
 cudaError_t run_low_rank(const AdapterCall& a, cudaStream_t s) {
   using L = LowRank<RP, TM, BWD>;
-  const AdapterPlanLayout P = adapter_plan_layout(*a.c, a.n);
-  uint8_t* p = static_cast<uint8_t*>(a.plan);
   // CTAs of a tile's cluster: as many as the SMs hold at a time
   const int tiles = max_tiles(a.c->T, a.n);
   const int most = std::min(ceil_div(a.K, L::KC), ceil_div(a.N, L::NC));
@@ -822,12 +774,7 @@ cudaError_t run_low_rank(const AdapterCall& a, cudaStream_t s) {
   const auto kern = low_rank_kernel<RP, TM, BWD>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::SMEM);
   if (e != cudaSuccess) return e;
-  const LowRankArgs g{a.in, a.W1, a.W2, a.scale, a.base, a.out, a.u, a.up, a.vp,
-                      reinterpret_cast<const int32_t*>(p + P.header),
-                      reinterpret_cast<const int32_t*>(p + P.rows),
-                      reinterpret_cast<const int4*>(p + P.tiles), reinterpret_cast<int32_t*>(p),
-                      a.c->T, a.n, a.r, a.K, a.N};
-  return launch_kernel(kern, (unsigned)tiles * cs, 256, L::SMEM, s, cs, g);
+  return launch_kernel(kern, (unsigned)tiles * cs, 256, L::SMEM, s, cs, low_rank_args(a));
 }
 
 template <int RP, bool BWD>
@@ -846,20 +793,25 @@ cudaError_t run_rank(const AdapterCall& a, cudaStream_t s) {
   }
 }
 
-template <int RP>
+template <int STAGES>
 cudaError_t run_grad(const GradArgs& g, cudaStream_t s) {
-  const auto kern = adapter_grad_kernel<RP>;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), Grad<RP>::SMEM);
+  const auto kern = adapter_grad_kernel<STAGES>;
+  const int smem = STAGES * g.stage_bytes + 1024 + kGradAux;
+  // the limit is set once per kernel: to the most any rank takes
+  const int most = STAGES * (STAGES == 6 ? 8 : 6) * kGradBox + 1024 + kGradAux;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), most);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(ceil_div(g.d, kGradCols) + ceil_div(g.d_out, kGradCols)),
                   (unsigned)(g.T / g.len + g.n + 1));
-  return launch_kernel(kern, grid, 256, Grad<RP>::SMEM, s, 0, g);
+  return launch_kernel(kern, grid, kGradThreads, smem, s, 0, g);
 }
 
 }  // namespace
 
 cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s) {
   if (a.c->T == 0) return cudaSuccess;
+  if (tile_rows(a.c->T, a.n) == 64 && a.c->T >= kTcRows)
+    return launch_low_rank_tc(low_rank_args(a), backward, max_tiles(a.c->T, a.n), s);
   return backward ? run_rank<true>(a, s) : run_rank<false>(a, s);
 }
 
@@ -874,6 +826,11 @@ cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan,
   const AdapterWsLayout W = adapter_ws_layout(c, n, r);
   uint8_t* p = static_cast<uint8_t*>(plan);
   uint8_t* w = static_cast<uint8_t*>(ws);
+  // The terms' boxes of 64 columns; two CTAs an SM by shared and tensor memory
+  // up to 256 columns (rank 80), one above.
+  const int N = ceil_div(3 * r, 16) * 16, boxes = ceil_div(N, 64);
+  int cols = 32;
+  while (cols < N) cols *= 2;
   const GradArgs g{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(dy),
                    reinterpret_cast<const __nv_bfloat16*>(w + W.u),
                    reinterpret_cast<const __nv_bfloat16*>(w + W.v), dA, dB,
@@ -881,14 +838,8 @@ cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan,
                    reinterpret_cast<const int32_t*>(p + P.header),
                    reinterpret_cast<const int32_t*>(p + P.offsets),
                    reinterpret_cast<const int32_t*>(p + P.rows), reinterpret_cast<int32_t*>(p),
-                   c.T, n, r, c.d, c.d_out, grad_len(c)};
-  cudaError_t e;
-  switch (rank_pad(r)) {
-    case 16: e = run_grad<16>(g, s); break;
-    case 32: e = run_grad<32>(g, s); break;
-    case 64: e = run_grad<64>(g, s); break;
-    default: e = run_grad<128>(g, s); break;
-  }
+                   c.T, n, r, c.d, c.d_out, grad_len(c), N, (2 + boxes) * kGradBox, cols};
+  cudaError_t e = boxes == 3 || boxes == 4 ? run_grad<4>(g, s) : run_grad<6>(g, s);
   if (e != cudaSuccess) return e;
   const int per = std::max(1, std::min(ceil_div((c.d + c.d_out) * r, 1024),
                                        ceil_div(8 * device_sm_count(), n)));
