@@ -370,19 +370,20 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
       for (int w = 0; w < L::TERMS; ++w) st_cluster_v2(dst + w * TM * RP * 2, tm[w]);
     }
     const int t = token(row);
-    if (t < 0 || j >= r) continue;
+    if (j >= r) continue;
     if (!BWD) {
-      if (g.u != nullptr)
+      if (t >= 0 && g.u != nullptr)
         *reinterpret_cast<float4*>(g.u + (size_t)t * r + j) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
       // the gradient's operands: v's and u's terms
-      const float4 uq = __ldg(reinterpret_cast<const float4*>(g.u + (size_t)t * r + j));
+      float4 uq = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t >= 0) uq = __ldg(reinterpret_cast<const float4*>(g.u + (size_t)t * r + j));
       const float uv[4] = {uq.x, uq.y, uq.z, uq.w};
       uint2 ut[3];
       split4<3>(uv, ut);
 #pragma unroll
       for (int w = 0; w < 3; ++w) {
-        const size_t o = ((size_t)t * 3 + w) * r + j;
+        const size_t o = (((size_t)(blockIdx.x / CS) * TM + row) * 3 + w) * r + j;
         *reinterpret_cast<uint2*>(g.vp + o) = tm[w < L::TERMS ? w : 0];
         *reinterpret_cast<uint2*>(g.up + o) = ut[w];
       }
@@ -494,8 +495,6 @@ __device__ __forceinline__ uint32_t grad_idesc(int n) {
 struct GradArgs {
   const __nv_bfloat16* x;   // (T, d)
   const __nv_bfloat16* dy;  // (T, d_out)
-  const __nv_bfloat16* up;  // (T, 3, r): u's three terms
-  const __nv_bfloat16* vp;  // (T, 3, r): v's
   float* dA;                // (n, d, r)
   float* dB;                // (n, r, d_out)
   float* part;              // (slots, r (d + d_out)): parts of split adapters, dA's then dB's
@@ -503,7 +502,7 @@ struct GradArgs {
   const int32_t* offsets;
   const int32_t* rows;
   int32_t* err;
-  int T, n, r, d, d_out, len;   // len: rows of a part, at most
+  int T, n, r, d, d_out, TM, len;   // TM: the plan's tile rows; len: rows of a part, at most
   int N, stage_bytes, tmem_cols;   // 3 r rounded up to 16; x's boxes and the terms'
 };
 
@@ -527,7 +526,9 @@ __device__ __forceinline__ int find_adapter(const int32_t* __restrict__ offsets,
 }
 
 template <int STAGES>
-__global__ void __launch_bounds__(kGradThreads, 2) adapter_grad_kernel(GradArgs g) {
+__global__ void __launch_bounds__(kGradThreads, 2)
+    adapter_grad_kernel(const __grid_constant__ CUtensorMap mapU,
+                        const __grid_constant__ CUtensorMap mapV, const GradArgs g) {
   pdl_wait_and_release();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -548,21 +549,23 @@ __global__ void __launch_bounds__(kGradThreads, 2) adapter_grad_kernel(GradArgs 
   const int o0 = __ldg(g.offsets + a), cnt = __ldg(g.offsets + a + 1) - o0;
   const int parts = ceil_div_dev(cnt, g.len), pi = slot - (o0 / g.len + a);
   if (pi >= parts) return;
-  const int r0 = o0 + (int)((long long)cnt * pi / parts);
-  const int nr = o0 + (int)((long long)cnt * (pi + 1) / parts) - r0;   // 1 .. len
+  // parts of equal length but for whole stages; none is empty
+  const int each = ceil_div_dev(ceil_div_dev(cnt, parts), kGradRows) * kGradRows;
+  const int i0 = pi * each, r0 = o0 + i0, nr = min(each, cnt - i0);   // 1 .. len
   const int mbx = ceil_div_dev(g.d, kGradCols);
   const bool isA = (int)blockIdx.x < mbx;
   const int m0 = (isA ? blockIdx.x : blockIdx.x - mbx) * kGradCols;
-  const int M = isA ? g.d : g.d_out, r = g.r, r3 = 3 * g.r;
+  const int M = isA ? g.d : g.d_out, r = g.r;
   const __nv_bfloat16* X = isA ? g.x : g.dy;
-  const __nv_bfloat16* V = isA ? g.vp : g.up;
+  const CUtensorMap* mapW = isA ? &mapV : &mapU;
+  const int w0 = (o0 / g.TM + a) * g.TM + i0;   // the part's first row of the terms
   for (int i = tid; i < nr; i += kGradThreads) s_rows[i] = __ldg(g.rows + r0 + i);
   if (warp == 4) {
     tmem_alloc(tmem_holder, (uint32_t)g.tmem_cols);
     tmem_relinquish();
     if (lane == 0) {
       for (int s = 0; s < STAGES; ++s) {
-        mbar_init(&full_bar[s], 128);  // each producer's copies
+        mbar_init(&full_bar[s], 129);  // each producer's copies, the terms' TMA
         mbar_init(&empty_bar[s], 1);   // the MMAs that read the stage
       }
       mbar_init(done_bar, 1);
@@ -577,8 +580,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) adapter_grad_kernel(GradArgs 
 
   if (warp < 4) {
     // ---- producers
-    const int nc = g.N / 8;
-    const int vrow = tid / 4;
+    const int boxes = g.stage_bytes / kGradBox - 2;
     bool alive = true;
     for (int s = 0; s < nst; ++s) {
       if (s >= STAGES) {
@@ -589,19 +591,20 @@ __global__ void __launch_bounds__(kGradThreads, 2) adapter_grad_kernel(GradArgs 
           break;
         }
       }
-      const uint32_t xs = smem_u32(smem + (s % STAGES) * g.stage_bytes), vs = xs + 2 * kGradBox;
+      uint8_t* stage = smem + (s % STAGES) * g.stage_bytes;
+      if (tid == 0) {
+        uint64_t* bar = &full_bar[s % STAGES];
+        mbar_arrive_expect_tx(bar, (uint32_t)(boxes * kGradBox));
+        for (int b = 0; b < boxes; ++b)
+          tma_load_3d(stage + (2 + b) * kGradBox, mapW, bar, b * 64, w0 + s * kGradRows, 0);
+      }
+      const uint32_t xs = smem_u32(stage);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = tid / 16 + 8 * i, c = tid % 16, col = m0 + c * 8, at = s * kGradRows + row;
         const bool ok = at < nr && col < M;
         cp_async16(xs + (c / 8) * kGradBox + tile_at<8>(row, c % 8),
                    ok ? X + (size_t)s_rows[at] * M + col : X, ok);
-      }
-      const int at = s * kGradRows + vrow;
-      const __nv_bfloat16* src = at < nr ? V + (size_t)s_rows[at] * r3 : V;
-      for (int c = tid % 4; c < nc; c += 4) {
-        const bool ok = at < nr && c * 8 < r3;
-        cp_async16(vs + (c / 8) * kGradBox + tile_at<8>(vrow, c % 8), ok ? src + c * 8 : V, ok);
       }
       cp_arrive(&full_bar[s % STAGES]);
     }
@@ -647,8 +650,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) adapter_grad_kernel(GradArgs 
       fence_proxy_async_smem();   // the copies' writes, before the tensor core reads them
       tc_fence_after_sync();
       const uint32_t xs = smem_u32(smem + (s % STAGES) * g.stage_bytes), vs = xs + 2 * kGradBox;
-#pragma unroll
-      for (int kk = 0; kk < kGradRows / 16; ++kk) {
+      // (the terms' rows behind the adapter's last tile are not its own)
+      const int steps = ceil_div_dev(min(kGradRows, nr - s * kGradRows), 16);
+      for (int kk = 0; kk < steps; ++kk) {
         const uint64_t ad = grad_desc(xs + kk * 2048);
         const uint32_t more = (s | kk) != 0 ? 1u : 0u;
         umma_bf16_ss(tmem, ad, grad_desc(vs + kk * 2048), grad_idesc(min(g.N, 256)), more);
@@ -700,9 +704,12 @@ int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 // so that they spread over the SMs and a tile is not mostly padding.
 int tile_rows(int T, int n) { return T <= 1024 || T <= 32 * n ? 16 : 64; }
 
-constexpr int kTcRows = 4096;
+constexpr int kTcRows = 4096, kTcRank = 33;
 
 int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
+
+// Rows of u's and v's terms: whole tiles.
+size_t term_rows(int T, int n) { return (size_t)max_tiles(T, n) * tile_rows(T, n); }
 
 // Rows of a part of the gradient's contraction, at most: one part for each CTA
 // that the SMs hold at a time (two an SM) were the adapters even.
@@ -731,7 +738,7 @@ AdapterWsLayout adapter_ws_layout(const moe_config_t& c, int n, int r) {
   AdapterWsLayout L{};
   const int len = grad_len(c);
   L.v = 0;
-  L.u = up256((size_t)c.T * r * 6);
+  L.u = up256(term_rows(c.T, n) * r * 6);
   L.part = 2 * L.u;
   // an adapter has several parts only if it has more rows than one takes
   const size_t slots = c.T > len ? (size_t)(c.T / len + n + 1) : 0;
@@ -794,23 +801,24 @@ cudaError_t run_rank(const AdapterCall& a, cudaStream_t s) {
 }
 
 template <int STAGES>
-cudaError_t run_grad(const GradArgs& g, cudaStream_t s) {
+cudaError_t run_grad(const CUtensorMap& mapU, const CUtensorMap& mapV, const GradArgs& g,
+                     cudaStream_t s) {
   const auto kern = adapter_grad_kernel<STAGES>;
   const int smem = STAGES * g.stage_bytes + 1024 + kGradAux;
   // the limit is set once per kernel: to the most any rank takes
-  const int most = STAGES * (STAGES == 6 ? 8 : 6) * kGradBox + 1024 + kGradAux;
+  const int most = STAGES * (STAGES == 6 ? 8 : STAGES == 5 ? 5 : 6) * kGradBox + 1024 + kGradAux;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), most);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(ceil_div(g.d, kGradCols) + ceil_div(g.d_out, kGradCols)),
                   (unsigned)(g.T / g.len + g.n + 1));
-  return launch_kernel(kern, grid, kGradThreads, smem, s, 0, g);
+  return launch_kernel(kern, grid, kGradThreads, smem, s, 0, mapU, mapV, g);
 }
 
 }  // namespace
 
 cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s) {
   if (a.c->T == 0) return cudaSuccess;
-  if (tile_rows(a.c->T, a.n) == 64 && a.c->T >= kTcRows)
+  if (tile_rows(a.c->T, a.n) == 64 && a.c->T >= kTcRows && a.r >= kTcRank)
     return launch_low_rank_tc(low_rank_args(a), backward, max_tiles(a.c->T, a.n), s);
   return backward ? run_rank<true>(a, s) : run_rank<false>(a, s);
 }
@@ -832,14 +840,21 @@ cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan,
   int cols = 32;
   while (cols < N) cols *= 2;
   const GradArgs g{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(dy),
-                   reinterpret_cast<const __nv_bfloat16*>(w + W.u),
-                   reinterpret_cast<const __nv_bfloat16*>(w + W.v), dA, dB,
+                   dA, dB,
                    reinterpret_cast<float*>(w + W.part),
                    reinterpret_cast<const int32_t*>(p + P.header),
                    reinterpret_cast<const int32_t*>(p + P.offsets),
                    reinterpret_cast<const int32_t*>(p + P.rows), reinterpret_cast<int32_t*>(p),
-                   c.T, n, r, c.d, c.d_out, grad_len(c), N, (2 + boxes) * kGradBox, cols};
-  cudaError_t e = boxes == 3 || boxes == 4 ? run_grad<4>(g, s) : run_grad<6>(g, s);
+                   c.T, n, r, c.d, c.d_out, tile_rows(c.T, n), grad_len(c), N,
+                   (2 + boxes) * kGradBox, cols};
+  CUtensorMap mapU, mapV;
+  const uint64_t rows = term_rows(c.T, n);
+  if (!encode_bf16(&mapU, w + W.u, 1, rows, 3 * (uint64_t)r, kGradRows) ||
+      !encode_bf16(&mapV, w + W.v, 1, rows, 3 * (uint64_t)r, kGradRows))
+    return cudaErrorNotSupported;
+  cudaError_t e = boxes == 4   ? run_grad<4>(mapU, mapV, g, s)
+                  : boxes == 3 ? run_grad<5>(mapU, mapV, g, s)
+                               : run_grad<6>(mapU, mapV, g, s);
   if (e != cudaSuccess) return e;
   const int per = std::max(1, std::min(ceil_div((c.d + c.d_out) * r, 1024),
                                        ceil_div(8 * device_sm_count(), n)));

@@ -116,7 +116,9 @@ struct LowRankArgs {
   const void* base;           // (T, N), bf16 forward, fp32 backward; null (0) or out
   void* out;                  // (T, N)
   float* u;                   // forward: (T, r) out or null; backward: the forward's
-  __nv_bfloat16* up;          // backward: u's and v's three terms out, (T, 3, r)
+  // backward: u's and v's three bf16 terms out, (tile slots x tile rows, 3, r),
+  // zeros in a tile's rows behind its last
+  __nv_bfloat16* up;
   __nv_bfloat16* vp;
   const int32_t* header;
   const int32_t* rows;
@@ -124,6 +126,22 @@ struct LowRankArgs {
   int32_t* err;
   int T, n, r, K, N;
 };
+
+// A bf16 tensor (outer, rows, cols) as a tensor map with a box of box_rows x
+// 64 columns (128 bytes: the swizzle's width); columns, rows and outer indices
+// outside read as zeros.
+inline bool encode_bf16(CUtensorMap* m, const void* ptr, uint64_t outer, uint64_t rows,
+                        uint64_t cols, uint32_t box_rows) {
+  if (tensor_map_encoder() == nullptr) return false;
+  const cuuint64_t dims[3] = {cols, rows, outer};
+  const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Low-rank products on tcgen05 (adapter_tc.cu) for tiles of 64 rows.
 cudaError_t launch_low_rank_tc(const LowRankArgs& g, bool backward, int tiles, cudaStream_t s);

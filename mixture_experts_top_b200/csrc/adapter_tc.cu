@@ -26,9 +26,11 @@ namespace {
 constexpr int kTm = 64;             // rows of a tile
 constexpr int kBlk = kTm * 128;     // 64 rows of 64 bf16 columns: 8 KiB
 constexpr int kKc = 128;            // input columns a stage
-constexpr int kProducers = 256;     // threads of the 8 producer warps
-constexpr int kMmaWarp = 16;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+// Warps: 0, 1, 4, 5 and 8, 9, 12, 13 epilogue (the two groups), 2, 3, 6, 7
+// row producers, 10 MMA issuer, 11 weight producer.
+constexpr int kProducers = 128;     // threads of the row producers
+constexpr int kMmaWarp = 10, kWeightWarp = 11;
+constexpr int kThreads = 32 * 14;
 constexpr int kFlush = 4;           // input stages a block of D1's sum
 constexpr int kAux = 1024;          // barriers, tmem address, rows
 constexpr int kMaxStages = 8;
@@ -81,7 +83,9 @@ TcShape tc_shape(int r) {
 }
 
 template <bool BWD>
-__global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g, TcShape sh) {
+__global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
+    const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+    const LowRankArgs g, const TcShape sh) {
   constexpr int TERMS = BWD ? 3 : 2;
   constexpr int OB = BWD ? 4 : 2;               // bytes of an output element
   constexpr int PV = 16 / OB;                   // output elements of 16 bytes
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
     tmem_relinquish();
     if (lane == 0) {
       for (int s = 0; s < sh.stages; ++s) {
-        mbar_init(&full[s], kProducers);   // each producer's copies
+        mbar_init(&full[s], kProducers + 1);   // each producer's copies, the weights' TMA
         mbar_init(&empty[s], 1);    // D1: the MMAs' completion; D2: the last epilogue warp
         left[s] = 0;
       }
@@ -145,6 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
       mbar_init(u_full, 4);
       mbar_init(drained, 1);
       fence_mbar_init();
+      tma_prefetch_map(&mapA);
+      tma_prefetch_map(&mapB);
     }
   }
   tc_fence_before_sync();
@@ -155,17 +161,43 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
   const int nf = ceil_div_dev(nk, kFlush);
   const int d1_col = sh.nb * 64, d2_col = 2 * d1_col;   // D1's second buffer, D2's first
 
-  const int role = warp == kMmaWarp ? 2 : (warp & 2) ? 0 : 1;   // producer, epilogue, MMA issuer
-  if (role == 0) {
-    // ------------------------------------------------------------ producers
+  if (warp == kWeightWarp) {
+    // ------------------------------------------------------ weight producer
+    int slot = 0;
+    uint32_t phase = 1;   // of the empty barriers; the first round waits for nothing
+    for (int s = 0; lane == 0 && s < nk + nn; ++s) {
+      if (s >= sh.stages && !mbar_wait(&empty[slot], phase)) {
+        report_error(g.err, kDevTimeoutProducer);
+        break;
+      }
+      uint8_t* ws = ring + slot * sh.stage + 2 * kBlk;
+      const int n0 = (s - nk) * NC;
+      mbar_arrive_expect_tx(&full[slot], (uint32_t)(s < nk ? sh.w1 : sh.w2));
+      if ((s < nk) != BWD) {
+        // A's rows, 64 at a time, in boxes of 64 of the rank's columns
+        const int row0 = BWD ? n0 : s * kKc;
+        for (int kb = 0; kb < (BWD ? 1 : 2); ++kb)
+          for (int j = 0; j < sh.nb; ++j)
+            tma_load_3d(ws + (kb * sh.nb + j) * kBlk, &mapA, &full[slot], j * 64, row0 + kb * 64,
+                        a);
+      } else {
+        // B's columns, 128 at a time, in boxes of 64
+        const int col0 = BWD ? s * kKc : n0;
+        for (int kb = 0; kb < 2; ++kb)
+          tma_load_3d(ws + kb * sh.rp * 128, &mapB, &full[slot], col0 + kb * 64, 0, a);
+      }
+      if (++slot == sh.stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp != kMmaWarp && (warp & 2) != 0) {
+    // -------------------------------------------------------- row producers
     const int p = ((warp >> 2) * 2 + (warp & 1)) * 32 + lane;   // 0 .. kProducers - 1
-    const __nv_bfloat16* w1 = g.W1 + (size_t)a * K * r;
-    const __nv_bfloat16* w2 = g.W2 + (size_t)a * N * r;
-    constexpr int R = kTm * 16 / kProducers;   // rows of a thread in a stage, 16 apart
+    constexpr int R = kTm * 16 / kProducers;   // rows of a thread in a stage, 8 apart
     int tok[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) tok[i] = s_rows[p / 16 + 16 * i];
-    const int rc = sh.rp / 8, inv = (65536 + rc - 1) / rc;   // i / rc = i inv >> 16, i < 4096
+    for (int i = 0; i < R; ++i) tok[i] = s_rows[p / 16 + 8 * i];
     const int total = nk + nn;
     int slot = 0;
     uint32_t phase = 1;   // of the empty barriers; the first round waits for nothing
@@ -183,51 +215,18 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const bool ok = tok[i] >= 0 && col < K;
-          cp_async16(st + (pc >> 3) * kBlk + tile_at<8>(p / 16 + 16 * i, pc & 7),
+          cp_async16(st + (pc >> 3) * kBlk + tile_at<8>(p / 16 + 8 * i, pc & 7),
                      ok ? g.in + (size_t)tok[i] * K + col : g.in, ok);
         }
-        const uint32_t ws = st + 2 * kBlk;
-        if (!BWD) {   // [k][j]
-          for (int i = p; i < kKc * rc; i += kProducers) {
-            const int row = i * inv >> 16, c = i - row * rc, k = s * kKc + row;
-            const bool in = k < K && c * 8 < r;
-            cp_async16(ws + ((row >> 6) * sh.nb + (c >> 3)) * kBlk + tile_at<8>(row & 63, c & 7),
-                       in ? w1 + (size_t)k * r + c * 8 : w1, in);
-          }
-        } else {      // [j][k]
-          for (int i = p; i < sh.rp * 16; i += kProducers) {
-            const int row = i >> 4, c = i & 15, k = s * kKc + c * 8;
-            const bool in = row < r && k < K;
-            cp_async16(ws + (c >> 3) * sh.rp * 128 + tile_at<8>(row, c & 7),
-                       in ? w1 + (size_t)row * K + k : w1, in);
-          }
-        }
       } else {
-        const int n0 = (s - nk) * NC;
-        const uint32_t ws = st + 2 * kBlk;
-        if (!BWD) {   // [j][c]
-          for (int i = p; i < sh.rp * 16; i += kProducers) {
-            const int row = i >> 4, c = i & 15, col = n0 + c * 8;
-            const bool in = row < r && col < N;
-            cp_async16(ws + (c >> 3) * sh.rp * 128 + tile_at<8>(row, c & 7),
-                       in ? w2 + (size_t)row * N + col : w2, in);
-          }
-        } else {      // [c][j]
-          for (int i = p; i < 64 * rc; i += kProducers) {
-            const int row = i * inv >> 16, c = i - row * rc;
-            const bool in = n0 + row < N && c * 8 < r;
-            cp_async16(ws + (c >> 3) * kBlk + tile_at<8>(row, c & 7),
-                       in ? w2 + (size_t)(n0 + row) * r + c * 8 : w2, in);
-          }
-        }
         const uint8_t* base = static_cast<const uint8_t*>(g.base);
-        const int col = n0 + pc * PV;
+        const int col = (s - nk) * NC + pc * PV;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const bool ok = tok[i] >= 0 && col < N && base != nullptr;
-          cp_async16(st + tile_at<BC>(p / 16 + 16 * i, pc),
+          cp_async16(st + tile_at<BC>(p / 16 + 8 * i, pc),
                      ok ? base + ((size_t)tok[i] * N + col) * OB
-                        : reinterpret_cast<const uint8_t*>(w2), ok);
+                        : reinterpret_cast<const uint8_t*>(g.in), ok);
         }
       }
       cp_arrive(&full[slot]);
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
       }
     }
     cp_wait_all();
-  } else if (role == 1) {
+  } else if (warp != kMmaWarp) {
     // ------------------------------------------------------------- epilogue
     // tensor-memory lane quarter, column half, and which output stages (every
     // other one); the second group joins for those alone
@@ -286,28 +285,30 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
         for (int w = 0; w < TERMS; ++w)
           *reinterpret_cast<uint4*>(smem + (w * sh.nb + cg / 8) * kBlk + tile_at<8>(row, cg % 8)) =
               make_uint4(lo[w].x, lo[w].y, hi[w].x, hi[w].y);
-        if (t >= 0) {
-          if (!BWD) {
-            if (g.u != nullptr) {
-              float4* o = reinterpret_cast<float4*>(g.u + (size_t)t * r + cg * 8);
-              o[0] = make_float4(v[0], v[1], v[2], v[3]);
-              o[1] = make_float4(v[4], v[5], v[6], v[7]);
-            }
-          } else {
-            // the gradient's operands: v's and u's terms
+        if (!BWD) {
+          if (t >= 0 && g.u != nullptr) {
+            float4* o = reinterpret_cast<float4*>(g.u + (size_t)t * r + cg * 8);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        } else {
+          // the gradient's operands: v's and u's terms
+          float4 u0 = make_float4(0.f, 0.f, 0.f, 0.f), u1 = u0;
+          if (t >= 0) {
             const float4* ui = reinterpret_cast<const float4*>(g.u + (size_t)t * r + cg * 8);
-            const float4 u0 = __ldg(ui), u1 = __ldg(ui + 1);
-            const float ua[4] = {u0.x, u0.y, u0.z, u0.w}, ub[4] = {u1.x, u1.y, u1.z, u1.w};
-            uint2 ulo[3], uhi[3];
-            split4<3>(ua, ulo);
-            split4<3>(ub, uhi);
+            u0 = __ldg(ui);
+            u1 = __ldg(ui + 1);
+          }
+          const float ua[4] = {u0.x, u0.y, u0.z, u0.w}, ub[4] = {u1.x, u1.y, u1.z, u1.w};
+          uint2 ulo[3], uhi[3];
+          split4<3>(ua, ulo);
+          split4<3>(ub, uhi);
 #pragma unroll
-            for (int w = 0; w < TERMS; ++w) {
-              const size_t o = ((size_t)t * 3 + w) * r + cg * 8;
-              *reinterpret_cast<uint4*>(g.vp + o) = make_uint4(lo[w].x, lo[w].y, hi[w].x, hi[w].y);
-              *reinterpret_cast<uint4*>(g.up + o) =
-                  make_uint4(ulo[w].x, ulo[w].y, uhi[w].x, uhi[w].y);
-            }
+          for (int w = 0; w < TERMS; ++w) {
+            const size_t o = (((size_t)blockIdx.x * kTm + row) * 3 + w) * r + cg * 8;
+            *reinterpret_cast<uint4*>(g.vp + o) = make_uint4(lo[w].x, lo[w].y, hi[w].x, hi[w].y);
+            *reinterpret_cast<uint4*>(g.up + o) =
+                make_uint4(ulo[w].x, ulo[w].y, uhi[w].x, uhi[w].y);
           }
         }
       }
@@ -321,15 +322,27 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
     fence_proxy_async_smem();
     __syncwarp();
     if (grp == 0 && alive && lane == 0) mbar_arrive(u_full);
+    // The rows this lane stores: 4 at a time, 8 lanes (128 bytes) each.
+    constexpr int HP = BC / 2;   // 16-byte pieces of this half's row
+    uint8_t* orow[HP];
+#pragma unroll
+    for (int k = 0; k < HP; ++k) {
+      const int tt = s_rows[q * 32 + k * 4 + lane / 8];
+      orow[k] = tt >= 0 ? static_cast<uint8_t*>(g.out) + (size_t)tt * N * OB : nullptr;
+    }
+    const int ocol = half * (NC / 2) + lane % 8 * PV;   // this lane's first column in a stage
     for (int i = grp; i < nn && alive; i += 2) {
       const int b = grp, slot = (nk + i) % sh.stages;
       const uint32_t fph = (uint32_t)((nk + i) / sh.stages) & 1u;
-      alive = mbar_wait(&d2_full[b], (uint32_t)(i >> 1) & 1u) && mbar_wait(&full[slot], fph);
+      alive = mbar_wait(&full[slot], fph) && mbar_wait(&d2_full[b], (uint32_t)(i >> 1) & 1u);
       alive = __all_sync(0xffffffffu, alive);
       if (!alive) break;
       tc_fence_after_sync();
       uint8_t* bs = ring + slot * sh.stage;
-      constexpr int HP = BC / 2;   // 16-byte pieces of this half's row
+      uint4 v[HP];
+#pragma unroll
+      for (int c = 0; c < HP; ++c)
+        v[c] = *reinterpret_cast<const uint4*>(bs + tile_at<BC>(row, half * HP + c));
 #pragma unroll
       for (int c0 = 0; c0 < HP; c0 += 32 / PV) {   // 32 columns at a time
         uint32_t d[32];
@@ -342,9 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
         }
 #pragma unroll
         for (int c = 0; c < 32 / PV; ++c) {
-          uint4* x = reinterpret_cast<uint4*>(bs + tile_at<BC>(row, half * HP + c0 + c));
-          uint4 v = *x;
-          uint32_t* w = &v.x;
+          uint32_t* w = &v[c0 + c].x;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             w[j] = BWD ? __float_as_uint(__uint_as_float(w[j]) + __uint_as_float(d[c * 4 + j]))
@@ -352,18 +363,21 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(LowRankArgs g,
                                          __uint_as_float(d[(c * 8 + 2 * j) & 31]),
                                      __uint_as_float(w[j] & 0xFFFF0000u) +
                                          __uint_as_float(d[(c * 8 + 2 * j + 1) & 31]));
-          *x = v;
         }
       }
+#pragma unroll
+      for (int c = 0; c < HP; ++c)
+        *reinterpret_cast<uint4*>(bs + tile_at<BC>(row, half * HP + c)) = v[c];
       __syncwarp();
 #pragma unroll
-      for (int k = 0; k < HP; ++k) {   // 32 / HP rows of the warp's at a time
-        const int rr = q * 32 + k * (32 / HP) + lane / HP, c = half * HP + lane % HP;
-        const int tt = s_rows[rr], col = i * NC + c * PV;
-        if (tt >= 0 && col < N)
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.out) + ((size_t)tt * N + col) * OB) =
-              *reinterpret_cast<const uint4*>(bs + tile_at<BC>(rr, c));
-      }
+      for (int k = 0; k < HP; ++k)
+        v[k] = *reinterpret_cast<const uint4*>(
+            bs + tile_at<BC>(q * 32 + k * 4 + lane / 8, half * HP + lane % 8));
+      const int col = i * NC + ocol;
+#pragma unroll
+      for (int k = 0; k < HP; ++k)
+        if (orow[k] != nullptr && col < N)
+          *reinterpret_cast<uint4*>(orow[k] + (size_t)col * OB) = v[k];
       __syncwarp();
       if (lane == 0) {   // the last of the four warps frees the stage
         __threadfence_block();
@@ -450,7 +464,11 @@ cudaError_t run(const LowRankArgs& g, int tiles, cudaStream_t s) {
   const auto kern = low_rank_tc_kernel<BWD>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), 227 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, (unsigned)tiles, kThreads, sh.smem, s, 0, g, sh);
+  CUtensorMap a, b;   // A (n, d, r) and B (n, r, d_out)
+  if (!encode_bf16(&a, BWD ? g.W2 : g.W1, g.n, BWD ? g.N : g.K, g.r, 64) ||
+      !encode_bf16(&b, BWD ? g.W1 : g.W2, g.n, g.r, BWD ? g.K : g.N, sh.rp))
+    return cudaErrorNotSupported;
+  return launch_kernel(kern, (unsigned)tiles, kThreads, sh.smem, s, 0, a, b, g, sh);
 }
 
 }  // namespace

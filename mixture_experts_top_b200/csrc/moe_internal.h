@@ -313,8 +313,8 @@ struct AdapterPlanLayout {
   size_t total;
 };
 AdapterPlanLayout adapter_plan_layout(const moe_config_t& c, int n);
-// v's and u's three bf16 terms (T, 3, r), and the parts of split adapters'
-// gradients.
+// v's and u's three bf16 terms (rows of whole tiles, 3, r), and the parts of
+// split adapters' gradients.
 struct AdapterWsLayout {
   size_t v, u, part, total;
 };
