@@ -41,10 +41,12 @@ constexpr int kPlanThreads = 1024;
 // own; after one exchange it writes its rows in token order.  A group's tiles
 // have the slots from offsets[g] / TM + g on, which no other group's have, so
 // that nothing needs the other groups' counts; slots left over hold no rows.
+// Rows stand by tile slot, -1 behind a tile's last, so that a kernel's CTA
+// reads its tile and its rows at once.
 __global__ void __launch_bounds__(kPlanThreads)
     adapter_plan_kernel(const int32_t* __restrict__ ids, int T, int n, int TM, int32_t* header,
                         int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
-                        int4* __restrict__ tiles, int32_t* err) {
+                        int2* __restrict__ tiles, int32_t* err) {
   pdl_wait_and_release();
   __shared__ int32_t s_less[32], s_mine[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x;
@@ -83,10 +85,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
   }
   const int slot0 = row0 / TM + g, nslots = (row0 + cnt) / TM + g + 1 - slot0;
+  rows += (size_t)slot0 * TM;
   for (int i = tid; i < nslots; i += kPlanThreads)
-    tiles[slot0 + i] = make_int4(g, row0 + i * TM, min(TM, max(0, cnt - i * TM)), 0);
+    tiles[slot0 + i] = make_int2(g, min(TM, max(0, cnt - i * TM)));
+  for (int i = cnt + tid; i < nslots * TM; i += kPlanThreads) rows[i] = -1;
   if (mine == 0) return;
-  int at = row0 + __reduce_add_sync(0xffffffffu, lane < warp ? s_mine[lane] : 0);
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? s_mine[lane] : 0);
 #pragma unroll 4
   for (int t = t0; t < t1; t += 32) {
     const bool in = t + lane < t1 && group(t + lane) == g;
@@ -142,23 +146,29 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
   const int CS = (int)cs, cr = (int)cluster_cta_rank();
   const int hT = __ldg(g.header), hn = __ldg(g.header + 1);
-  const int4 tl = __ldg(g.tiles + blockIdx.x / CS);
-  const int r = g.r, K = g.K, N = g.N, a = tl.x, nrows = tl.z;
+  const int tile = blockIdx.x / CS;
+  const int2 tl = __ldg(g.tiles + tile);
+  // The token of tile row i, -1 behind the last.
+  auto token = [&](int i) { return __ldg(g.rows + (size_t)tile * TM + i); };
+  constexpr int PV = 16 / L::OB;           // output elements of 16 bytes
+  constexpr int BC = L::NC / PV;           // 16-byte pieces of a stage's output row
+  constexpr int BR = TM * BC / 256;        // output rows of a thread in a stage
+  constexpr int XC = L::KC / 8;            // 16-byte pieces of a stage's input row
+  constexpr int XR = TM * XC / 256;        // input rows of a thread in a stage
+  int bt[BR], xt[XR];
+#pragma unroll
+  for (int i = 0; i < BR; ++i) bt[i] = token(tid / BC + i * (256 / BC));
+#pragma unroll
+  for (int i = 0; i < XR; ++i) xt[i] = token(tid / XC + i * (256 / XC));
+  const int r = g.r, K = g.K, N = g.N, a = tl.x;
   if (hT != g.T || hn != g.n) {   // the same for every CTA
     if (tid == 0) report_error(g.err, kDevBadPlan);
     return;
   }
-  if (nrows == 0) return;         // the same for the cluster
-  // The token of tile row i, -1 behind the last.
-  auto token = [&](int i) { return i < nrows ? __ldg(g.rows + tl.y + i) : -1; };
+  if (tl.y == 0) return;          // no rows: the same for the cluster
+  const float sc = a < g.n ? __ldg(g.scale + a) : 0.f;
   const int nn = ceil_div_dev(N, L::NC);
   const int n0 = (int)((long long)nn * cr / CS), n1 = (int)((long long)nn * (cr + 1) / CS);
-  constexpr int PV = 16 / L::OB;           // output elements of 16 bytes
-  constexpr int BC = L::NC / PV;           // 16-byte pieces of a stage's output row
-  constexpr int BR = TM * BC / 256;        // output rows of a thread in a stage
-  int bt[BR];
-#pragma unroll
-  for (int i = 0; i < BR; ++i) bt[i] = token(tid / BC + i * (256 / BC));
   if (a == g.n) {   // rows without an adapter: out = base
     if (g.base == g.out) return;
     for (int nc = n0; nc < n1; ++nc) {
@@ -180,14 +190,9 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
   // ---- loads ----
   const int nk = ceil_div_dev(K, L::KC);
   const int k0 = (int)((long long)nk * cr / CS), k1 = (int)((long long)nk * (cr + 1) / CS);
-  constexpr int XC = L::KC / 8;            // 16-byte pieces of a stage's input row
-  constexpr int XR = TM * XC / 256;        // input rows of a thread in a stage
   const __nv_bfloat16* xrow[XR];
 #pragma unroll
-  for (int i = 0; i < XR; ++i) {
-    const int t = token(tid / XC + i * (256 / XC));
-    xrow[i] = t >= 0 ? g.in + (size_t)t * K : nullptr;
-  }
+  for (int i = 0; i < XR; ++i) xrow[i] = xt[i] >= 0 ? g.in + (size_t)xt[i] * K : nullptr;
   auto load_w1 = [&](int kc) {
     const uint32_t ws = ring + (uint32_t)((kc - k0) % L::ST1) * L::S1 + TM * L::KC * 2;
     if (!BWD) {   // [k][j]
@@ -344,12 +349,14 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
   }
   if (CS > 1) cluster_sync_all();
   else __syncthreads();
-  // Each CTA adds its share of the rows over the cluster and hands the bf16
-  // terms to every CTA's operand tile.
-  const float sc = __ldg(g.scale + a);
-  const int e0 = TM * cr / CS * RP, e1 = TM * (cr + 1) / CS * RP;
+  // Few rows: every CTA adds all of them over the cluster, which spares it a
+  // second barrier.  Many: each adds its share and hands the bf16 terms to
+  // every CTA's operand tile.
+  const int own0 = TM * cr / CS, own1 = TM * (cr + 1) / CS;
+  const int e0 = (L::AHEAD ? 0 : own0) * RP, e1 = (L::AHEAD ? TM : own1) * RP;
   for (int i = e0 + tid * 4; i < e1; i += 1024) {
     const int row = i / RP, j = i % RP;
+    const int t = token(row);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int q = 0; q < CS; ++q) {
       const float4 p = CS > 1 ? ld_cluster_f4(cluster_smem_addr(partp + i, (uint32_t)q))
@@ -364,13 +371,18 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
     uint2 tm[L::TERMS];
     split4<L::TERMS>(v, tm);
     const uint32_t at = L::RING + tile_at<RP / 8>(row, j / 8) + (j % 8) * 2;
-    for (int q = 0; q < CS; ++q) {
-      const uint32_t dst = CS > 1 ? cluster_smem_addr(smem + at, (uint32_t)q) : ring + at;
+    if (L::AHEAD || CS == 1) {
 #pragma unroll
-      for (int w = 0; w < L::TERMS; ++w) st_cluster_v2(dst + w * TM * RP * 2, tm[w]);
+      for (int w = 0; w < L::TERMS; ++w)
+        *reinterpret_cast<uint2*>(smem + at + w * TM * RP * 2) = tm[w];
+    } else {
+      for (int q = 0; q < CS; ++q) {
+        const uint32_t dst = cluster_smem_addr(smem + at, (uint32_t)q);
+#pragma unroll
+        for (int w = 0; w < L::TERMS; ++w) st_cluster_v2(dst + w * TM * RP * 2, tm[w]);
+      }
     }
-    const int t = token(row);
-    if (j >= r) continue;
+    if (j >= r || row < own0 || row >= own1) continue;
     if (!BWD) {
       if (t >= 0 && g.u != nullptr)
         *reinterpret_cast<float4*>(g.u + (size_t)t * r + j) = make_float4(v[0], v[1], v[2], v[3]);
@@ -383,14 +395,14 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
       split4<3>(uv, ut);
 #pragma unroll
       for (int w = 0; w < 3; ++w) {
-        const size_t o = (((size_t)(blockIdx.x / CS) * TM + row) * 3 + w) * r + j;
+        const size_t o = (((size_t)tile * TM + row) * 3 + w) * r + j;
         *reinterpret_cast<uint2*>(g.vp + o) = tm[w < L::TERMS ? w : 0];
         *reinterpret_cast<uint2*>(g.up + o) = ut[w];
       }
     }
   }
-  if (CS > 1) cluster_sync_all();
-  else __syncthreads();
+  if (L::AHEAD || CS == 1) __syncthreads();
+  else cluster_sync_all();
 
   // ---- second product: out[rows, slice] = base + u W2[:, slice] ----
   const int w2n = warp / L::WM;
@@ -460,6 +472,7 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
                                             tile_at<BC>(tid / BC + i * (256 / BC), tid % BC));
   }
   cp_wait<0>();
+  if (L::AHEAD && CS > 1) cluster_sync_all();   // peers have read this CTA's partial sums
 }
 
 // --------------------------------------------------------------- gradient --
@@ -551,15 +564,15 @@ __global__ void __launch_bounds__(kGradThreads, 2)
   if (pi >= parts) return;
   // parts of equal length but for whole stages; none is empty
   const int each = ceil_div_dev(ceil_div_dev(cnt, parts), kGradRows) * kGradRows;
-  const int i0 = pi * each, r0 = o0 + i0, nr = min(each, cnt - i0);   // 1 .. len
+  const int i0 = pi * each, nr = min(each, cnt - i0);   // 1 .. len
   const int mbx = ceil_div_dev(g.d, kGradCols);
   const bool isA = (int)blockIdx.x < mbx;
   const int m0 = (isA ? blockIdx.x : blockIdx.x - mbx) * kGradCols;
   const int M = isA ? g.d : g.d_out, r = g.r;
   const __nv_bfloat16* X = isA ? g.x : g.dy;
   const CUtensorMap* mapW = isA ? &mapV : &mapU;
-  const int w0 = (o0 / g.TM + a) * g.TM + i0;   // the part's first row of the terms
-  for (int i = tid; i < nr; i += kGradThreads) s_rows[i] = __ldg(g.rows + r0 + i);
+  const int w0 = (o0 / g.TM + a) * g.TM + i0;   // the part's first row, by tile slot
+  for (int i = tid; i < nr; i += kGradThreads) s_rows[i] = __ldg(g.rows + w0 + i);
   if (warp == 4) {
     tmem_alloc(tmem_holder, (uint32_t)g.tmem_cols);
     tmem_relinquish();
@@ -708,7 +721,7 @@ constexpr int kTcRows = 4096, kTcRank = 33;
 
 int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
 
-// Rows of u's and v's terms: whole tiles.
+// Rows by tile slot (the plan's, and u's and v's terms): whole tiles.
 size_t term_rows(int T, int n) { return (size_t)max_tiles(T, n) * tile_rows(T, n); }
 
 // Rows of a part of the gradient's contraction, at most: one part for each CTA
@@ -729,8 +742,8 @@ AdapterPlanLayout adapter_plan_layout(const moe_config_t& c, int n) {
   L.header = 64;   // cleared by moe_workspace_init: a plan not made fits no call
   L.offsets = 256;
   L.rows = L.offsets + up256((size_t)(n + 2) * 4);
-  L.tiles = L.rows + up256((size_t)c.T * 4);
-  L.total = L.tiles + up256((size_t)max_tiles(c.T, n) * 16);
+  L.tiles = L.rows + up256(term_rows(c.T, n) * 4);
+  L.total = L.tiles + up256((size_t)max_tiles(c.T, n) * 8);
   return L;
 }
 
@@ -754,7 +767,7 @@ cudaError_t launch_adapter_plan(const moe_config_t& c, int n, const int32_t* ids
                        tile_rows(c.T, n), reinterpret_cast<int32_t*>(p + L.header),
                        reinterpret_cast<int32_t*>(p + L.offsets),
                        reinterpret_cast<int32_t*>(p + L.rows),
-                       reinterpret_cast<int4*>(p + L.tiles), reinterpret_cast<int32_t*>(p));
+                       reinterpret_cast<int2*>(p + L.tiles), reinterpret_cast<int32_t*>(p));
 }
 
 namespace {
@@ -765,7 +778,7 @@ LowRankArgs low_rank_args(const AdapterCall& a) {
   return LowRankArgs{a.in, a.W1, a.W2, a.scale, a.base, a.out, a.u, a.up, a.vp,
                      reinterpret_cast<const int32_t*>(p + P.header),
                      reinterpret_cast<const int32_t*>(p + P.rows),
-                     reinterpret_cast<const int4*>(p + P.tiles), reinterpret_cast<int32_t*>(p),
+                     reinterpret_cast<const int2*>(p + P.tiles), reinterpret_cast<int32_t*>(p),
                      a.c->T, a.n, a.r, a.K, a.N};
 }
 

@@ -122,7 +122,7 @@ struct LowRankArgs {
   __nv_bfloat16* vp;
   const int32_t* header;
   const int32_t* rows;
-  const int4* tiles;
+  const int2* tiles;
   int32_t* err;
   int T, n, r, K, N;
 };

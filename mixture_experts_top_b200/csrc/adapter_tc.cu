@@ -110,14 +110,14 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   int32_t* s_rows = reinterpret_cast<int32_t*>(aux + 512);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hT = __ldg(g.header), hn = __ldg(g.header + 1);
-  const int4 tl = __ldg(g.tiles + blockIdx.x);
-  const int r = g.r, K = g.K, N = g.N, a = tl.x, nrows = tl.z;
+  const int2 tl = __ldg(g.tiles + blockIdx.x);
+  if (tid < kTm) s_rows[tid] = __ldg(g.rows + (size_t)blockIdx.x * kTm + tid);
+  const int r = g.r, K = g.K, N = g.N, a = tl.x, nrows = tl.y;
   if (hT != g.T || hn != g.n) {
     if (tid == 0) report_error(g.err, kDevBadPlan);
     return;
   }
   if (nrows == 0) return;
-  if (tid < kTm) s_rows[tid] = tid < nrows ? __ldg(g.rows + tl.y + tid) : -1;
   if (a == g.n) {   // rows without an adapter: out = base
     if (g.base == g.out) return;
     __syncthreads();
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     // this thread's columns of u: groups of 8, [g0, g1)
     const int g0 = half == 0 ? 0 : (r / 8 + 1) / 2, g1 = half == 0 ? (r / 8 + 1) / 2 : r / 8;
+    const float sc = __ldg(g.scale + a);
     float acc[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -269,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(&d1_empty[f & 1]);
     }
-    const float sc = __ldg(g.scale + a);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int cg = g0 + i;   // 8 columns: a 16-byte piece of u's terms

@@ -308,8 +308,8 @@ struct AdapterPlanLayout {
   size_t ctrl;      // error word (256 bytes, the header in them)
   size_t header;    // int32: T, n, tiles
   size_t offsets;   // (n + 2) int32: rows of adapter a; group n: no adapter
-  size_t rows;      // (T) int32: tokens by group, in token order
-  size_t tiles;     // int4: group, first row, rows
+  size_t rows;      // int32: tokens by group, in token order, by tile slot (-1: none)
+  size_t tiles;     // int2: group, rows
   size_t total;
 };
 AdapterPlanLayout adapter_plan_layout(const moe_config_t& c, int n);
