@@ -481,16 +481,25 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
 // terms side by side on the MMA's N, so that X is read from shared memory once
 // for all of them; the epilogue adds a row's three column groups.  Both
 // operands run down their rows on the contraction (MN-major, 128-byte swizzle:
-// boxes of 64 columns x 32 rows).  Warps 0-3 gather rows into the stages by
-// cp.async, then read tensor memory; warp 4 issues the MMAs.
+// boxes of 64 columns x 32 rows).
+// The rows, by tile slot, are cut into equal chunks, as many as give every SM
+// two CTAs, whatever the adapters' sizes; a CTA walks the adapters that meet its
+// chunk.  One that lies in it whole goes straight to the gradient; the part of
+// another in chunk p goes to the slot p + a, which no other part has, and the
+// last launch adds an adapter's parts in order.  (One CTA per adapter and part
+// instead ran in two uneven waves: 33 us against MEASURED at 8192 x 2048, rank
+// 64.)
+// Warps 0-3 read tensor memory, 4-7 gather x's rows into the stages by
+// cp.async, 8 issues the MMAs, 9 loads the terms by TMA (its issue would hold
+// up the rows' if they shared a warp).
 constexpr int kGradCols = 128;   // columns of x (dA) or dy (dB) a CTA: the MMA's M
 constexpr int kGradRows = 32;    // rows a stage
-// Rows of a part, at most: the tensor core's fp32 sums of 1024 rows keep the
+// Rows of a chunk, at most: the tensor core's fp32 sums of 1024 rows keep the
 // gradients within 8e-7 of exact, normwise; the parts are added in
 // round-to-nearest fp32.
 constexpr int kGradMax = 1024;
 constexpr int kGradBox = kGradRows * 128;           // 64 bf16 columns of a stage's rows
-constexpr int kGradThreads = 160;
+constexpr int kGradThreads = 320;
 constexpr int kGradAux = 1024 + kGradMax * 4;       // barriers, tmem address, rows
 
 // The MN-major descriptor: boxes along MN kGradBox apart, 8-row groups 1024
@@ -515,21 +524,51 @@ struct GradArgs {
   const int32_t* offsets;
   const int32_t* rows;
   int32_t* err;
-  int T, n, r, d, d_out, TM, len;   // TM: the plan's tile rows; len: rows of a part, at most
+  int T, n, r, d, d_out, TM, chunks;   // TM: the plan's tile rows
   int N, stage_bytes, tmem_cols;   // 3 r rounded up to 16; x's boxes and the terms'
 };
 
-// An adapter of c rows has ceil(c / len) parts of equal length; part i of
-// adapter a has the slot offsets[a] / len + a + i, which no other part has.
-// The adapter of a slot: the last a with offsets[a] / len + a <= slot.
-__device__ __forceinline__ int find_adapter(const int32_t* __restrict__ offsets, int n, int len,
-                                            int slot) {
+// Adapter a's first row by tile slot.
+__device__ __forceinline__ int first_row(const GradArgs& g, int a) {
+  return (__ldg(g.offsets + a) / g.TM + a) * g.TM;
+}
+// Rows of a chunk: the adapters' tile slots in g.chunks equal parts, in whole
+// stages.
+__device__ __forceinline__ int chunk_rows(const GradArgs& g) {
+  return ceil_div_dev(ceil_div_dev(first_row(g, g.n), g.chunks), kGradRows) * kGradRows;
+}
+
+// The parts of a chunk in order: rows [i0, i1) of adapter a, whose first row by
+// tile slot is at `at`.
+struct ChunkParts {
+  const GradArgs& g;
+  int lo, hi, a, at, i0, i1;
+  bool whole;   // all of the adapter's rows
+  // a0: the last adapter that starts at or before the chunk
+  __device__ ChunkParts(const GradArgs& g_, int lo_, int hi_, int a0)
+      : g(g_), lo(lo_), hi(hi_), a(a0 - 1) {}
+  __device__ bool next() {
+    while (++a < g.n) {
+      const int o = __ldg(g.offsets + a), cnt = __ldg(g.offsets + a + 1) - o;
+      at = (o / g.TM + a) * g.TM;
+      if (at >= hi) return false;
+      i0 = max(0, lo - at);
+      i1 = min(cnt, hi - at);
+      whole = i0 == 0 && i1 == cnt;
+      if (i0 < i1) return true;
+    }
+    return false;
+  }
+};
+
+// The last adapter a with first_row(a) <= row, or -1; by a converged warp.
+__device__ __forceinline__ int find_adapter(const GradArgs& g, int row) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;   // the answer + 1 is in [lo, hi]
+  int lo = 0, hi = g.n;   // the answer + 1 is in [lo, hi]
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
-    const bool le = i < hi && __ldg(offsets + i) / len + i <= slot;
+    const bool le = i < hi && first_row(g, i) <= row;
     const int c = __popc(__ballot_sync(0xffffffffu, le));
     if (c == 0) break;
     hi = min(hi, lo + c * step);
@@ -541,39 +580,43 @@ __device__ __forceinline__ int find_adapter(const int32_t* __restrict__ offsets,
 template <int STAGES>
 __global__ void __launch_bounds__(kGradThreads, 2)
     adapter_grad_kernel(const __grid_constant__ CUtensorMap mapU,
-                        const __grid_constant__ CUtensorMap mapV, const GradArgs g) {
+                        const __grid_constant__ CUtensorMap mapV,
+                        const __grid_constant__ GradArgs g) {
   pdl_wait_and_release();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + STAGES * g.stage_bytes);
   uint64_t* empty_bar = full_bar + STAGES;
-  uint64_t* done_bar = empty_bar + STAGES;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
+  uint64_t* d_full = empty_bar + STAGES;
+  uint64_t* d_empty = d_full + 1;
+  uint64_t* drained = d_empty + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   int32_t* s_rows = reinterpret_cast<int32_t*>(smem + STAGES * g.stage_bytes + 256);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (__ldg(g.header) != g.T || __ldg(g.header + 1) != g.n) {
     if (tid == 0) report_error(g.err, kDevBadPlan);
     return;
   }
-  const int slot = blockIdx.y;
-  const int a = find_adapter(g.offsets, g.n, g.len, slot);
-  if (a < 0) return;
-  const int o0 = __ldg(g.offsets + a), cnt = __ldg(g.offsets + a + 1) - o0;
-  const int parts = ceil_div_dev(cnt, g.len), pi = slot - (o0 / g.len + a);
-  if (pi >= parts) return;
-  // parts of equal length but for whole stages; none is empty
-  const int each = ceil_div_dev(ceil_div_dev(cnt, parts), kGradRows) * kGradRows;
-  const int i0 = pi * each, nr = min(each, cnt - i0);   // 1 .. len
-  const int mbx = ceil_div_dev(g.d, kGradCols);
-  const bool isA = (int)blockIdx.x < mbx;
-  const int m0 = (isA ? blockIdx.x : blockIdx.x - mbx) * kGradCols;
+  const int mbx = ceil_div_dev(g.d, kGradCols), mbs = mbx + ceil_div_dev(g.d_out, kGradCols);
+  const int chunk = blockIdx.x / mbs, mb = blockIdx.x - chunk * mbs;
+  const int len = chunk_rows(g), lo = chunk * len;
+  const int hi = min(lo + len, first_row(g, g.n));   // (T <= 2^30: no overflow)
+  if (lo >= hi) return;
+  // the chunk's rows are on their way while its first adapter is found
+  constexpr int PRE = (kGradMax + kGradThreads - 1) / kGradThreads;
+  int pre[PRE];
+#pragma unroll
+  for (int k = 0; k < PRE; ++k)
+    pre[k] = tid + k * kGradThreads < hi - lo ? __ldg(g.rows + lo + tid + k * kGradThreads) : -1;
+  const int a0 = max(0, find_adapter(g, lo));
+  const bool isA = mb < mbx;
+  const int m0 = (isA ? mb : mb - mbx) * kGradCols;
   const int M = isA ? g.d : g.d_out, r = g.r;
-  const __nv_bfloat16* X = isA ? g.x : g.dy;
-  const CUtensorMap* mapW = isA ? &mapV : &mapU;
-  const int w0 = (o0 / g.TM + a) * g.TM + i0;   // the part's first row, by tile slot
-  for (int i = tid; i < nr; i += kGradThreads) s_rows[i] = __ldg(g.rows + w0 + i);
-  if (warp == 4) {
+#pragma unroll
+  for (int k = 0; k < PRE; ++k)
+    if (tid + k * kGradThreads < kGradMax) s_rows[tid + k * kGradThreads] = pre[k];
+  if (warp == 8) {
     tmem_alloc(tmem_holder, (uint32_t)g.tmem_cols);
     tmem_relinquish();
     if (lane == 0) {
@@ -581,7 +624,9 @@ __global__ void __launch_bounds__(kGradThreads, 2)
         mbar_init(&full_bar[s], 129);  // each producer's copies, the terms' TMA
         mbar_init(&empty_bar[s], 1);   // the MMAs that read the stage
       }
-      mbar_init(done_bar, 1);
+      mbar_init(d_full, 1);
+      mbar_init(d_empty, 4);           // the epilogue warps
+      mbar_init(drained, 1);
       fence_mbar_init();
     }
   }
@@ -589,97 +634,152 @@ __global__ void __launch_bounds__(kGradThreads, 2)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
-  const int nst = ceil_div_dev(nr, kGradRows);
+  ChunkParts part(g, lo, hi, a0);
 
-  if (warp < 4) {
+  if (warp >= 4 && warp < 8) {
     // ---- producers
-    const int boxes = g.stage_bytes / kGradBox - 2;
+    const __nv_bfloat16* X = isA ? g.x : g.dy;
+    const int p = tid - 128, c = p % 16, col = m0 + c * 8;
+    // rows 8 apart: the swizzle is the same for all four
+    const uint32_t dst = (uint32_t)(c / 8) * kGradBox + tile_at<8>(p / 16, c % 8);
     bool alive = true;
-    for (int s = 0; s < nst; ++s) {
-      if (s >= STAGES) {
-        alive = mbar_wait(&empty_bar[s % STAGES], (uint32_t)(s / STAGES - 1) & 1u);
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) {
-          report_error(g.err, kDevTimeoutProducer);
-          break;
-        }
-      }
-      uint8_t* stage = smem + (s % STAGES) * g.stage_bytes;
-      if (tid == 0) {
+    for (int s = 0; alive && part.next();) {
+      for (int i = part.i0; i < part.i1; i += kGradRows, ++s) {
         uint64_t* bar = &full_bar[s % STAGES];
-        mbar_arrive_expect_tx(bar, (uint32_t)(boxes * kGradBox));
-        for (int b = 0; b < boxes; ++b)
-          tma_load_3d(stage + (2 + b) * kGradBox, mapW, bar, b * 64, w0 + s * kGradRows, 0);
-      }
-      const uint32_t xs = smem_u32(stage);
+        if (s >= STAGES) {
+          alive = mbar_wait(&empty_bar[s % STAGES], (uint32_t)(s / STAGES - 1) & 1u);
+          alive = __all_sync(0xffffffffu, alive);
+          if (!alive) {
+            report_error(g.err, kDevTimeoutProducer);
+            break;
+          }
+        }
+        uint8_t* stage = smem + (s % STAGES) * g.stage_bytes;
+        const uint32_t xs = smem_u32(stage);
+        const __nv_bfloat16* src[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = tid / 16 + 8 * i, c = tid % 16, col = m0 + c * 8, at = s * kGradRows + row;
-        const bool ok = at < nr && col < M;
-        cp_async16(xs + (c / 8) * kGradBox + tile_at<8>(row, c % 8),
-                   ok ? X + (size_t)s_rows[at] * M + col : X, ok);
+        for (int k = 0; k < 4; ++k) {
+          const int at = i + p / 16 + 8 * k;
+          src[k] = at < part.i1 && col < M ? X + (size_t)s_rows[part.at + at - lo] * M + col
+                                           : nullptr;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          cp_async16(dst + xs + k * 8 * 128, src[k] != nullptr ? src[k] : X, src[k] != nullptr);
+        cp_arrive(bar);
       }
-      cp_arrive(&full_bar[s % STAGES]);
     }
     cp_wait_all();
+  } else if (warp < 4) {
     // ---- epilogue: lane = column of x, tensor-memory columns = the three terms
-    const bool ready = __all_sync(0xffffffffu, alive && mbar_wait(done_bar, 0));
-    if (alive && !ready) report_error(g.err, kDevTimeoutEpilogue);
-    tc_fence_after_sync();
     const size_t dsz = (size_t)g.d * r, bsz = (size_t)g.d_out * r;
-    // the adapter's only part goes straight to the gradient
-    float* out = parts == 1 ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
-                            : g.part + (size_t)slot * (dsz + bsz) + (isA ? 0 : dsz);
     const int m = m0 + warp * 32 + lane;
     const uint32_t acc = tmem + ((uint32_t)(warp * 32) << 16);
-    for (int j = 0; ready && j < r; j += 8) {
-      uint32_t t0[8], t1[8], t2[8];
-      tmem_ld_32x32b_x8(acc + (uint32_t)j, t0);
-      tmem_ld_32x32b_x8(acc + (uint32_t)(r + j), t1);
-      tmem_ld_32x32b_x8(acc + (uint32_t)(2 * r + j), t2);
-      tmem_ld_wait();
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = __uint_as_float(t0[i]) + (__uint_as_float(t1[i]) + __uint_as_float(t2[i]));
-      if (m >= M) continue;
-      if (isA) {
-        float4* o = reinterpret_cast<float4*>(out + (size_t)m * r + j);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) out[(size_t)(j + i) * M + m] = v[i];
-      }
-    }
-    tc_fence_before_sync();
-  } else if (lane == 0) {
-    // ---- MMA issuer
-    for (int s = 0; s < nst; ++s) {
-      if (!mbar_wait(&full_bar[s % STAGES], (uint32_t)(s / STAGES) & 1u)) {
-        report_error(g.err, kDevTimeoutMma);
+    uint32_t ph = 0;
+    while (part.next()) {
+      if (!__all_sync(0xffffffffu, mbar_wait(d_full, ph))) {
+        report_error(g.err, kDevTimeoutEpilogue);
         break;
       }
-      fence_proxy_async_smem();   // the copies' writes, before the tensor core reads them
+      ph ^= 1u;
       tc_fence_after_sync();
-      const uint32_t xs = smem_u32(smem + (s % STAGES) * g.stage_bytes), vs = xs + 2 * kGradBox;
-      // (the terms' rows behind the adapter's last tile are not its own)
-      const int steps = ceil_div_dev(min(kGradRows, nr - s * kGradRows), 16);
-      for (int kk = 0; kk < steps; ++kk) {
-        const uint64_t ad = grad_desc(xs + kk * 2048);
-        const uint32_t more = (s | kk) != 0 ? 1u : 0u;
-        umma_bf16_ss(tmem, ad, grad_desc(vs + kk * 2048), grad_idesc(min(g.N, 256)), more);
-        if (g.N > 256)
-          umma_bf16_ss(tmem + 256, ad, grad_desc(vs + 4 * kGradBox + kk * 2048),
-                       grad_idesc(g.N - 256), more);
+      const int a = part.a;
+      float* out = part.whole
+                       ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
+                       : g.part + (size_t)(chunk + a) * (dsz + bsz) + (isA ? 0 : dsz);
+      for (int j0 = 0; j0 < r; j0 += 16) {
+        uint32_t t[2][3][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (j0 + 8 * h < r)
+#pragma unroll
+            for (int w = 0; w < 3; ++w)
+              tmem_ld_32x32b_x8(acc + (uint32_t)(w * r + j0 + 8 * h), t[h][w]);
+        tmem_ld_wait();
+        if (j0 + 16 >= r) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(d_empty);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = j0 + 8 * h;
+          if (j >= r || m >= M) continue;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = __uint_as_float(t[h][0][i]) +
+                   (__uint_as_float(t[h][1][i]) + __uint_as_float(t[h][2][i]));
+          if (isA) {
+            float4* o = reinterpret_cast<float4*>(out + (size_t)m * r + j);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[(size_t)(j + i) * M + m] = v[i];
+          }
+        }
       }
-      umma_commit(&empty_bar[s % STAGES]);
     }
-    umma_commit(done_bar);
-    if (!mbar_wait(done_bar, 0)) report_error(g.err, kDevTimeoutDrain);
+  } else if (warp == 9) {
+    // ---- the terms
+    const CUtensorMap* terms = isA ? &mapV : &mapU;
+    const int boxes = g.stage_bytes / kGradBox - 2;
+    bool alive = lane == 0;
+    for (int s = 0; alive && part.next();) {
+      for (int i = part.i0; i < part.i1; i += kGradRows, ++s) {
+        uint64_t* bar = &full_bar[s % STAGES];
+        if (s >= STAGES) {
+          alive = mbar_wait(&empty_bar[s % STAGES], (uint32_t)(s / STAGES - 1) & 1u);
+          if (!alive) {
+            report_error(g.err, kDevTimeoutProducer);
+            break;
+          }
+        }
+        uint8_t* stage = smem + (s % STAGES) * g.stage_bytes;
+        mbar_arrive_expect_tx(bar, (uint32_t)(boxes * kGradBox));
+        for (int b = 0; b < boxes; ++b)
+          tma_load_3d(stage + (2 + b) * kGradBox, terms, bar, b * 64, part.at + i, 0);
+      }
+    }
+  } else {
+    // ---- MMA issuer: the whole warp runs the loop, one lane issues
+    auto wait = [](uint64_t* bar, uint32_t ph) {
+      return (bool)__all_sync(0xffffffffu, mbar_wait(bar, ph));
+    };
+    bool alive = true;
+    int s = 0, q = 0;
+    for (; alive && part.next(); ++q) {
+      if (q > 0) alive = wait(d_empty, (uint32_t)(q - 1) & 1u);
+      tc_fence_after_sync();
+      uint32_t more = 0;
+      for (int i = part.i0; alive && i < part.i1; i += kGradRows, ++s) {
+        alive = wait(&full_bar[s % STAGES], (uint32_t)(s / STAGES) & 1u);
+        if (!alive) break;
+        fence_proxy_async_smem();   // the copies' writes, before the tensor core reads them
+        tc_fence_after_sync();
+        const uint32_t xs = smem_u32(smem + (s % STAGES) * g.stage_bytes), vs = xs + 2 * kGradBox;
+        // (the terms' rows behind the adapter's last tile are not its own)
+        const int steps = ceil_div_dev(min(kGradRows, part.i1 - i), 16);
+        for (int kk = 0; kk < steps; ++kk) {
+          const uint64_t ad = grad_desc(xs + kk * 2048);
+          umma_elect(tmem, ad, grad_desc(vs + kk * 2048), grad_idesc(min(g.N, 256)), more);
+          if (g.N > 256)
+            umma_elect(tmem + 256, ad, grad_desc(vs + 4 * kGradBox + kk * 2048),
+                       grad_idesc(g.N - 256), more);
+          more = 1;
+        }
+        umma_commit_elect(&empty_bar[s % STAGES]);
+      }
+      umma_commit_elect(d_full);
+    }
+    if (!alive) report_error(g.err, kDevTimeoutMma);
+    umma_commit_elect(drained);
+    if (!wait(drained, 0)) report_error(g.err, kDevTimeoutDrain);
   }
+  tc_fence_before_sync();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, (uint32_t)g.tmem_cols);
   }
@@ -690,11 +790,12 @@ __global__ void __launch_bounds__(256) adapter_reduce_kernel(GradArgs g) {
   pdl_wait_and_release();
   if (__ldg(g.header) != g.T || __ldg(g.header + 1) != g.n) return;
   const int a = blockIdx.y;
-  const int o0 = __ldg(g.offsets + a), cnt = __ldg(g.offsets + a + 1) - o0;
-  const int parts = ceil_div_dev(cnt, g.len);
+  const int at = first_row(g, a), cnt = __ldg(g.offsets + a + 1) - __ldg(g.offsets + a);
+  const int len = chunk_rows(g), p0 = len > 0 ? at / len : 0;
+  const int parts = cnt > 0 ? (at + cnt - 1) / len - p0 + 1 : 0;
   if (parts == 1) return;
   const size_t dsz = (size_t)g.d * g.r, bsz = (size_t)g.d_out * g.r, all = dsz + bsz;
-  const float* src = g.part + (size_t)(o0 / g.len + a) * all;
+  const float* src = g.part + (size_t)(p0 + a) * all;
   for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all;
        i += (size_t)gridDim.x * 1024) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -717,19 +818,27 @@ int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 // so that they spread over the SMs and a tile is not mostly padding.
 int tile_rows(int T, int n) { return T <= 1024 || T <= 32 * n ? 16 : 64; }
 
-constexpr int kTcRows = 4096, kTcRank = 33;
-
 int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
+
+// Whether the low-rank products run on tcgen05, a CTA (and an SM) to a tile of
+// 64 rows: where the tiles give work to more than half of the SMs.  Fewer tiles
+// are shared by clusters of CTAs on mma.sync instead.  Forward and backward on
+// B200, us (tcgen05 against mma.sync): 8192 rows of 2048, rank 64, 113 / 132;
+// of 4096, rank 16, 167 / 186; 6000 of 1024, rank 128, 104 / 126; but 4096 of
+// 2048, rank 64, 99 / 87, and 2048 of 4096 149 / 112.
+bool use_tc(int T, int n) { return tile_rows(T, n) == 64 && T / 64 > device_sm_count() / 2; }
 
 // Rows by tile slot (the plan's, and u's and v's terms): whole tiles.
 size_t term_rows(int T, int n) { return (size_t)max_tiles(T, n) * tile_rows(T, n); }
 
-// Rows of a part of the gradient's contraction, at most: one part for each CTA
-// that the SMs hold at a time (two an SM) were the adapters even.
-int grad_len(const moe_config_t& c) {
-  const int64_t mb = ceil_div(c.d, kGradCols) + ceil_div(c.d_out, kGradCols);
-  const int64_t rows = (c.T * mb + 2 * 148 - 1) / (2 * 148);
-  return (int)std::min<int64_t>(kGradMax, std::max<int64_t>(256, (rows + 31) / 32 * 32));
+// Chunks of the gradient's rows: two CTAs an SM, but 256 rows at least (a part's
+// trip through memory costs more) and kGradMax at most.
+int grad_chunks(const moe_config_t& c, int n) {
+  const int mb = ceil_div(c.d, kGradCols) + ceil_div(c.d_out, kGradCols);
+  const int64_t rows = (int64_t)term_rows(c.T, n);
+  const int even = (int)std::min<int64_t>(2 * device_sm_count() / mb, rows / 256);
+  return std::max(std::max(1, even), (int)((rows + kGradMax - kGradRows - 1) /
+                                           (kGradMax - kGradRows)));
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -749,13 +858,10 @@ AdapterPlanLayout adapter_plan_layout(const moe_config_t& c, int n) {
 
 AdapterWsLayout adapter_ws_layout(const moe_config_t& c, int n, int r) {
   AdapterWsLayout L{};
-  const int len = grad_len(c);
   L.v = 0;
   L.u = up256(term_rows(c.T, n) * r * 6);
   L.part = 2 * L.u;
-  // an adapter has several parts only if it has more rows than one takes
-  const size_t slots = c.T > len ? (size_t)(c.T / len + n + 1) : 0;
-  L.total = L.part + up256(slots * (size_t)r * ((size_t)c.d + c.d_out) * 4) + 256;
+  L.total = L.part + up256((size_t)(grad_chunks(c, n) + n) * r * ((size_t)c.d + c.d_out) * 4);
   return L;
 }
 
@@ -822,8 +928,8 @@ cudaError_t run_grad(const CUtensorMap& mapU, const CUtensorMap& mapV, const Gra
   const int most = STAGES * (STAGES == 6 ? 8 : STAGES == 5 ? 5 : 6) * kGradBox + 1024 + kGradAux;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), most);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(ceil_div(g.d, kGradCols) + ceil_div(g.d_out, kGradCols)),
-                  (unsigned)(g.T / g.len + g.n + 1));
+  const unsigned grid =
+      (unsigned)(ceil_div(g.d, kGradCols) + ceil_div(g.d_out, kGradCols)) * (unsigned)g.chunks;
   return launch_kernel(kern, grid, kGradThreads, smem, s, 0, mapU, mapV, g);
 }
 
@@ -831,7 +937,7 @@ cudaError_t run_grad(const CUtensorMap& mapU, const CUtensorMap& mapV, const Gra
 
 cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s) {
   if (a.c->T == 0) return cudaSuccess;
-  if (tile_rows(a.c->T, a.n) == 64 && a.c->T >= kTcRows && a.r >= kTcRank)
+  if (use_tc(a.c->T, a.n))
     return launch_low_rank_tc(low_rank_args(a), backward, max_tiles(a.c->T, a.n), s);
   return backward ? run_rank<true>(a, s) : run_rank<false>(a, s);
 }
@@ -858,7 +964,7 @@ cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan,
                    reinterpret_cast<const int32_t*>(p + P.header),
                    reinterpret_cast<const int32_t*>(p + P.offsets),
                    reinterpret_cast<const int32_t*>(p + P.rows), reinterpret_cast<int32_t*>(p),
-                   c.T, n, r, c.d, c.d_out, tile_rows(c.T, n), grad_len(c), N,
+                   c.T, n, r, c.d, c.d_out, tile_rows(c.T, n), grad_chunks(c, n), N,
                    (2 + boxes) * kGradBox, cols};
   CUtensorMap mapU, mapV;
   const uint64_t rows = term_rows(c.T, n);

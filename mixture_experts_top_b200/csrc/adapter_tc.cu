@@ -26,11 +26,13 @@ namespace {
 constexpr int kTm = 64;             // rows of a tile
 constexpr int kBlk = kTm * 128;     // 64 rows of 64 bf16 columns: 8 KiB
 constexpr int kKc = 128;            // input columns a stage
-// Warps: 0, 1, 4, 5 and 8, 9, 12, 13 epilogue (the two groups), 2, 3, 6, 7
-// row producers, 10 MMA issuer, 11 weight producer.
-constexpr int kProducers = 128;     // threads of the row producers
-constexpr int kMmaWarp = 10, kWeightWarp = 11;
-constexpr int kThreads = 32 * 14;
+// Warps: those with warp % 4 in {0, 1} (tensor memory's lanes 0-63) are the
+// epilogue, four to a group: 12 of them.  Of the others 8 load rows, one issues
+// the MMAs, one loads the weights and two idle.
+constexpr int kGroups = 3;
+constexpr int kThreads = 32 * 8 * kGroups;
+constexpr int kProducers = 256;     // threads of the row producers
+constexpr int kMmaWarp = 18, kWeightWarp = 19;
 constexpr int kFlush = 4;           // input stages a block of D1's sum
 constexpr int kAux = 1024;          // barriers, tmem address, rows
 constexpr int kMaxStages = 8;
@@ -61,7 +63,7 @@ struct TcShape {
   int stages;
   int u_bytes;     // the terms of u
   int smem;
-  int cols;        // tensor-memory columns: D1 twice, D2 twice
+  int groups;      // epilogue groups that take output stages, a D2 buffer each
 };
 
 template <bool BWD>
@@ -78,7 +80,7 @@ TcShape tc_shape(int r) {
   // + kBlk: the MMA's upper rows of the last stage
   t.stages = std::min(kMaxStages, (224 * 1024 - 1024 - kAux - kBlk - t.u_bytes) / t.stage);
   t.smem = t.stages * t.stage + t.u_bytes + kBlk + kAux + 1024;
-  t.cols = 512;
+  t.groups = std::min(kGroups, (512 - 2 * t.nb * 64) / (BWD ? 64 : 128));
   return t;
 }
 
@@ -101,9 +103,9 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   uint64_t* empty = full + kMaxStages;
   uint64_t* d1_full = empty + kMaxStages;       // [2]
   uint64_t* d1_empty = d1_full + 2;
-  uint64_t* d2_full = d1_empty + 2;
-  uint64_t* d2_empty = d2_full + 2;
-  uint64_t* u_full = d2_empty + 2;
+  uint64_t* d2_full = d1_empty + 2;             // [kGroups]
+  uint64_t* d2_empty = d2_full + kGroups;
+  uint64_t* u_full = d2_empty + kGroups;
   uint64_t* drained = u_full + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   int32_t* left = reinterpret_cast<int32_t*>(aux + 384);   // epilogue warps done with a stage
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
     return;
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(tmem_holder, (uint32_t)sh.cols);
+    tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
     if (lane == 0) {
       for (int s = 0; s < sh.stages; ++s) {
@@ -142,11 +144,13 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       }
       for (int b = 0; b < 2; ++b) {
         mbar_init(&d1_full[b], 1);
-        mbar_init(&d1_empty[b], 4);   // the epilogue warps
-        mbar_init(&d2_full[b], 1);
-        mbar_init(&d2_empty[b], 4);
+        mbar_init(&d1_empty[b], 4 * kGroups);   // the epilogue warps
       }
-      mbar_init(u_full, 4);
+      for (int b = 0; b < kGroups; ++b) {
+        mbar_init(&d2_full[b], 1);
+        mbar_init(&d2_empty[b], 4);             // the group's warps
+      }
+      mbar_init(u_full, 4 * kGroups);
       mbar_init(drained, 1);
       fence_mbar_init();
       tma_prefetch_map(&mapA);
@@ -191,13 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
         phase ^= 1u;
       }
     }
-  } else if (warp != kMmaWarp && (warp & 2) != 0) {
+  } else if ((warp & 2) != 0 && warp < 2 * kProducers / 32) {
     // -------------------------------------------------------- row producers
     const int p = ((warp >> 2) * 2 + (warp & 1)) * 32 + lane;   // 0 .. kProducers - 1
-    constexpr int R = kTm * 16 / kProducers;   // rows of a thread in a stage, 8 apart
+    constexpr int R = kTm * 16 / kProducers;   // rows of a thread in a stage, 16 apart
     int tok[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) tok[i] = s_rows[p / 16 + 8 * i];
+    for (int i = 0; i < R; ++i) tok[i] = s_rows[p / 16 + 16 * i];
     const int total = nk + nn;
     int slot = 0;
     uint32_t phase = 1;   // of the empty barriers; the first round waits for nothing
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const bool ok = tok[i] >= 0 && col < K;
-          cp_async16(st + (pc >> 3) * kBlk + tile_at<8>(p / 16 + 8 * i, pc & 7),
+          cp_async16(st + (pc >> 3) * kBlk + tile_at<8>(p / 16 + 16 * i, pc & 7),
                      ok ? g.in + (size_t)tok[i] * K + col : g.in, ok);
         }
       } else {
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const bool ok = tok[i] >= 0 && col < N && base != nullptr;
-          cp_async16(st + tile_at<BC>(p / 16 + 8 * i, pc),
+          cp_async16(st + tile_at<BC>(p / 16 + 16 * i, pc),
                      ok ? base + ((size_t)tok[i] * N + col) * OB
                         : reinterpret_cast<const uint8_t*>(g.in), ok);
         }
@@ -236,31 +240,32 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       }
     }
     cp_wait_all();
-  } else if (warp != kMmaWarp) {
+  } else if ((warp & 2) == 0) {
     // ------------------------------------------------------------- epilogue
-    // tensor-memory lane quarter, column half, and which output stages (every
-    // other one); the second group joins for those alone
+    // tensor-memory lane quarter, half of an output stage's columns, group
     const int q = warp & 1, half = (warp >> 2) & 1, grp = warp >> 3;
     const int row = q * 32 + lane, t = s_rows[row];
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    // this thread's columns of u: groups of 8, [g0, g1)
-    const int g0 = half == 0 ? 0 : (r / 8 + 1) / 2, g1 = half == 0 ? (r / 8 + 1) / 2 : r / 8;
+    // This thread's columns of u, 8 at a time: every (2 kGroups)-th piece.
+    constexpr int PU = (kAdapterMaxRank / 8 + 2 * kGroups - 1) / (2 * kGroups);
+    const int p0 = warp >> 2;
     const float sc = __ldg(g.scale + a);
-    float acc[8][8];
+    float acc[PU][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < PU; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     bool alive = true;
-    for (int f = 0; grp == 0 && f < nf && alive; ++f) {
+    for (int f = 0; f < nf && alive; ++f) {
       alive = __all_sync(0xffffffffu, mbar_wait(&d1_full[f & 1], (uint32_t)(f >> 1) & 1u));
       if (!alive) break;
       tc_fence_after_sync();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (g0 + i < g1) {
+      for (int i = 0; i < PU; ++i) {
+        const int cg = p0 + i * 2 * kGroups;
+        if (cg * 8 < r) {
           uint32_t d[8];
-          tmem_ld_32x32b_x8(lanes + (uint32_t)((f & 1) * d1_col + (g0 + i) * 8), d);
+          tmem_ld_32x32b_x8(lanes + (uint32_t)((f & 1) * d1_col + cg * 8), d);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[i][j] += __uint_as_float(d[j]);
@@ -271,9 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       if (lane == 0) mbar_arrive(&d1_empty[f & 1]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int cg = g0 + i;   // 8 columns: a 16-byte piece of u's terms
-      if (grp == 0 && cg < g1) {
+    for (int i = 0; i < PU; ++i) {
+      const int cg = p0 + i * 2 * kGroups;   // 8 columns: a 16-byte piece of u's terms
+      if (cg * 8 < r) {
         uint2 lo[TERMS], hi[TERMS];
         float v[8];
 #pragma unroll
@@ -311,17 +316,16 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
                 make_uint4(ulo[w].x, ulo[w].y, uhi[w].x, uhi[w].y);
           }
         }
-      }
-    }
-    if (grp == 0 && half == 1 && r % 16 != 0) {   // columns behind an odd rank: zeros
+      } else if (cg * 8 < sh.rp) {   // columns behind an odd rank: zeros
 #pragma unroll
-      for (int w = 0; w < TERMS; ++w)
-        *reinterpret_cast<uint4*>(smem + (w * sh.nb + r / 64) * kBlk + tile_at<8>(row, r / 8 % 8)) =
-            make_uint4(0, 0, 0, 0);
+        for (int w = 0; w < TERMS; ++w)
+          *reinterpret_cast<uint4*>(smem + (w * sh.nb + cg / 8) * kBlk + tile_at<8>(row, cg % 8)) =
+              make_uint4(0, 0, 0, 0);
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (grp == 0 && alive && lane == 0) mbar_arrive(u_full);
+    if (alive && lane == 0) mbar_arrive(u_full);
     // The rows this lane stores: 4 at a time, 8 lanes (128 bytes) each.
     constexpr int HP = BC / 2;   // 16-byte pieces of this half's row
     uint8_t* orow[HP];
@@ -331,31 +335,31 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       orow[k] = tt >= 0 ? static_cast<uint8_t*>(g.out) + (size_t)tt * N * OB : nullptr;
     }
     const int ocol = half * (NC / 2) + lane % 8 * PV;   // this lane's first column in a stage
-    for (int i = grp; i < nn && alive; i += 2) {
-      const int b = grp, slot = (nk + i) % sh.stages;
+    const uint32_t acc2 = lanes + (uint32_t)(d2_col + grp * NC + half * (NC / 2));
+    int use = 0;   // stages this group has taken
+    for (int i = grp; grp < sh.groups && i < nn && alive; i += sh.groups, ++use) {
+      const int slot = (nk + i) % sh.stages;
       const uint32_t fph = (uint32_t)((nk + i) / sh.stages) & 1u;
-      alive = mbar_wait(&full[slot], fph) && mbar_wait(&d2_full[b], (uint32_t)(i >> 1) & 1u);
+      alive = mbar_wait(&full[slot], fph) && mbar_wait(&d2_full[grp], (uint32_t)use & 1u);
       alive = __all_sync(0xffffffffu, alive);
       if (!alive) break;
       tc_fence_after_sync();
       uint8_t* bs = ring + slot * sh.stage;
-      uint4 v[HP];
-#pragma unroll
-      for (int c = 0; c < HP; ++c)
-        v[c] = *reinterpret_cast<const uint4*>(bs + tile_at<BC>(row, half * HP + c));
 #pragma unroll
       for (int c0 = 0; c0 < HP; c0 += 32 / PV) {   // 32 columns at a time
         uint32_t d[32];
-        tmem_ld_32x32b_x32(lanes + (uint32_t)(d2_col + b * NC + half * (NC / 2) + c0 * PV), d);
+        tmem_ld_32x32b_x32(acc2 + (uint32_t)(c0 * PV), d);
         tmem_ld_wait();
         if (c0 + 32 / PV >= HP) {
           tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&d2_empty[b]);
+          if (lane == 0) mbar_arrive(&d2_empty[grp]);
         }
 #pragma unroll
         for (int c = 0; c < 32 / PV; ++c) {
-          uint32_t* w = &v[c0 + c].x;
+          uint4* x = reinterpret_cast<uint4*>(bs + tile_at<BC>(row, half * HP + c0 + c));
+          uint4 v = *x;
+          uint32_t* w = &v.x;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             w[j] = BWD ? __float_as_uint(__uint_as_float(w[j]) + __uint_as_float(d[c * 4 + j]))
@@ -363,21 +367,16 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
                                          __uint_as_float(d[(c * 8 + 2 * j) & 31]),
                                      __uint_as_float(w[j] & 0xFFFF0000u) +
                                          __uint_as_float(d[(c * 8 + 2 * j + 1) & 31]));
+          *x = v;
         }
       }
-#pragma unroll
-      for (int c = 0; c < HP; ++c)
-        *reinterpret_cast<uint4*>(bs + tile_at<BC>(row, half * HP + c)) = v[c];
       __syncwarp();
-#pragma unroll
-      for (int k = 0; k < HP; ++k)
-        v[k] = *reinterpret_cast<const uint4*>(
-            bs + tile_at<BC>(q * 32 + k * 4 + lane / 8, half * HP + lane % 8));
       const int col = i * NC + ocol;
 #pragma unroll
       for (int k = 0; k < HP; ++k)
         if (orow[k] != nullptr && col < N)
-          *reinterpret_cast<uint4*>(orow[k] + (size_t)col * OB) = v[k];
+          *reinterpret_cast<uint4*>(orow[k] + (size_t)col * OB) = *reinterpret_cast<const uint4*>(
+              bs + tile_at<BC>(q * 32 + k * 4 + lane / 8, half * HP + lane % 8));
       __syncwarp();
       if (lane == 0) {   // the last of the four warps frees the stage
         __threadfence_block();
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       }
     }
     if (!alive) report_error(g.err, kDevTimeoutEpilogue);
-  } else {
+  } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------- MMA issuer
     // the whole warp runs the loop; one lane issues
     auto wait = [](uint64_t* bar, uint32_t ph) {
@@ -422,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
     }
     alive = alive && wait(u_full, 0);
     const uint32_t us = smem_u32(smem);
+    int b = 0, use = 0;   // output stage i: group b, its use-th
     for (int i = 0; i < nn && alive; ++i) {
-      const int b = i & 1;
-      if (i >= 2) alive = wait(&d2_empty[b], (uint32_t)(i / 2 - 1) & 1u);
+      if (use > 0) alive = wait(&d2_empty[b], (uint32_t)(use - 1) & 1u);
       alive = alive && wait(&full[slot], fph);
       if (!alive) break;
       fence_proxy_async_smem();
@@ -441,6 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
           more = 1;
         }
       umma_commit_elect(&d2_full[b]);
+      if (++b == sh.groups) {
+        b = 0;
+        ++use;
+      }
       if (++slot == sh.stages) {
         slot = 0;
         fph ^= 1u;
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, (uint32_t)sh.cols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
