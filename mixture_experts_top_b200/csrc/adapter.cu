@@ -16,9 +16,10 @@
 //            the r-wide partial sums meet through distributed shared memory
 //            in CTA order, and each writes its slice of the output's columns;
 //            u never makes a trip through HBM between the products.
-// gradient - rows of an adapter on the contraction, 128 columns of x or dy a
-//            CTA; long adapters are split at fixed row positions and their
-//            parts added in order by a last launch.  No floating-point
+//            (Many rows: adapter_tc.cu, one CTA per tile on tcgen05.)
+// gradient - on tcgen05, rows of an adapter on the contraction, 128 columns of
+//            x or dy a CTA; the rows are cut into equal chunks and the parts of
+//            a cut adapter added in order by a last launch.  No floating-point
 //            atomics anywhere.
 //
 // Precision: bf16 operands, fp32 sums.  The tensor core adds one staged block
@@ -487,8 +488,7 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
 // chunk.  One that lies in it whole goes straight to the gradient; the part of
 // another in chunk p goes to the slot p + a, which no other part has, and the
 // last launch adds an adapter's parts in order.  (One CTA per adapter and part
-// instead ran in two uneven waves: 33 us against MEASURED at 8192 x 2048, rank
-// 64.)
+// instead ran in two uneven waves: 33 us against 25 at 8192 x 2048, rank 64.)
 // Warps 0-3 read tensor memory, 4-7 gather x's rows into the stages by
 // cp.async, 8 issues the MMAs, 9 loads the terms by TMA (its issue would hold
 // up the rows' if they shared a warp).

@@ -84,8 +84,9 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint2 v) {
 }
 
 // tcgen05.mma and its commit, issued by one elected lane of a warp that runs
-// its loop converged: the descriptors then stay in uniform registers.  (From
-// a loop of one lane alone an issue cost 50 ns and bounded the kernels.)
+// its loop converged: the descriptors then stay in uniform registers.  With A
+// in shared memory an MMA of M = 128, K = 16 takes 40 cycles for N = 16, 49 for
+// 64, 65 for 128 and 129 for 256, measured: A's read is its floor.
 __device__ __forceinline__ void umma_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -95,6 +96,28 @@ __device__ __forceinline__ void umma_elect(uint32_t d_tmem, uint64_t a_desc, uin
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// The same with A in tensor memory: lane = row, a 32-bit column = two
+// neighbouring k.
+__device__ __forceinline__ void umma_elect_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// This warp's 32 lanes, 4 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, uint32_t a, uint32_t b,
+                                                  uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
   asm volatile(

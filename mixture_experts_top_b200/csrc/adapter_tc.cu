@@ -2,19 +2,24 @@
 // of many rows (adapter.cu has the formulas, the plan and the other forms).
 //
 // One CTA per tile of 64 rows of one adapter, both products in one launch:
-//   D1 (64, r)  = in[rows, :] W1         input columns 64 at a time
-//   u           = scale D1, split into bf16 terms, written to shared memory
-//   D2 (64, 64) = sum over the terms of u_w W2[:, 64 columns]; out = base + D2
-// Warps 2, 3, 6, 7 gather the rows and load the weights by cp.async, input
-// columns first and then base's, through ONE ring of stages: while u is formed
-// the second product's loads are already in flight, so HBM never waits.  Warp
-// 8 issues the MMAs (M = 128: the upper 64 rows read whatever follows in
-// shared memory and are never looked at).  Warps 0, 1, 4, 5 own the tensor
-// memory's lanes 0-63 (two halves of the columns each): they add D1's blocks
-// of 512 input columns in round-to-nearest fp32 (the tensor core's own sums
-// truncate), and write D2 through the stage's base tile, so that every global
-// access of a warp covers whole sectors.
-// Bound by HBM: 2 (K + 2 N) bytes a row forward, 2 K + 8 N backward.
+//   D1 (64, r)  = in[rows, :] W1         input columns 128 at a time
+//   u           = scale D1, split into bf16 terms, written to tensor memory
+//   D2 (64, NC) = sum over the terms of u_w W2[:, NC columns]; out = base + D2
+// with NC = 128 columns of bf16 forward, 64 of fp32 backward.  8 warps gather
+// the rows by cp.async (input columns first and then base's) and one loads the
+// weights by TMA, all through ONE ring of stages: while u is formed the second
+// product's loads are already in flight, so HBM never waits.  One warp issues
+// the MMAs (M = 128: the upper 64 rows read whatever follows in shared memory,
+// or stands in tensor memory, and are never looked at).  The second product
+// takes u's terms from tensor memory: an MMA of 128 x 64 x 16 whose A is in
+// shared memory takes 49 cycles, 37 of them A's read.  The warps that own
+// tensor memory's lanes 0-63 are the epilogue: three groups, an output stage and
+// a D2 buffer each in turn.  They add D1's blocks in round-to-nearest fp32 (the
+// tensor core's own sums truncate), and write D2 through the stage's base tile,
+// so that every global access of a warp covers whole sectors.  u's terms reach
+// the second product before what later launches need is written out.
+// Bound by HBM: 2 (K + 2 N) bytes a row forward, 2 K + 8 N backward.  B200, 8192
+// rows, 8 adapters: forward MEASF, backward MEASB.
 // Every wait is bounded (moe_device.cuh) and recorded on the error word.
 #include "adapter.cuh"
 #include "moe_device.cuh"
@@ -33,7 +38,11 @@ constexpr int kGroups = 3;
 constexpr int kThreads = 32 * 8 * kGroups;
 constexpr int kProducers = 256;     // threads of the row producers
 constexpr int kMmaWarp = 18, kWeightWarp = 19;
-constexpr int kFlush = 4;           // input stages a block of D1's sum
+// Input stages a block of D1's sum: the truncation of 256 columns' sums leaves u
+// and v within 2e-7 of exact, 512's within 4e-7, which u's and v's products, the
+// gradients, would show; blocks of 1024 are 1-2 % faster and serve a forward
+// pass that keeps no u, whose output is bf16.
+constexpr int kFlushKept = 2, kFlush = 8;
 constexpr int kAux = 1024;          // barriers, tmem address, rows
 constexpr int kMaxStages = 8;
 
@@ -61,13 +70,14 @@ struct TcShape {
   int w1, w2;      // bytes of a stage's W1, W2 part (multiples of 1024)
   int stage;       // bytes of a stage
   int stages;
-  int u_bytes;     // the terms of u
   int smem;
+  int u_col, d2_col;   // tensor-memory columns
   int groups;      // epilogue groups that take output stages, a D2 buffer each
+  int flush;       // input stages a block of D1's sum
 };
 
 template <bool BWD>
-TcShape tc_shape(int r) {
+TcShape tc_shape(int r, bool kept) {
   TcShape t;
   t.rp = ceil_div(r, 16) * 16;
   t.nb = ceil_div(t.rp, 64);
@@ -76,12 +86,28 @@ TcShape tc_shape(int r) {
   t.w1 = BWD ? 2 * t.rp * 128 : 2 * t.nb * kBlk;
   t.w2 = BWD ? t.nb * kBlk : 2 * t.rp * 128;
   t.stage = 2 * kBlk + std::max(t.w1, t.w2);
-  t.u_bytes = (BWD ? 3 : 2) * t.nb * kBlk;
   // + kBlk: the MMA's upper rows of the last stage
-  t.stages = std::min(kMaxStages, (224 * 1024 - 1024 - kAux - kBlk - t.u_bytes) / t.stage);
-  t.smem = t.stages * t.stage + t.u_bytes + kBlk + kAux + 1024;
-  t.groups = std::min(kGroups, (512 - 2 * t.nb * 64) / (BWD ? 64 : 128));
+  t.stages = std::min(kMaxStages, (224 * 1024 - 1024 - kAux - kBlk) / t.stage);
+  t.smem = t.stages * t.stage + kBlk + kAux + 1024;
+  // tensor memory: D1, u's terms (two bf16 a column), a D2 for each group
+  t.u_col = t.nb * 64;
+  t.d2_col = t.u_col + (BWD ? 3 : 2) * t.rp / 2;
+  t.groups = std::min(kGroups, (512 - t.d2_col) / (BWD ? 64 : 128));
+  t.flush = kept ? kFlushKept : kFlush;
   return t;
+}
+
+// The three bf16 terms of 8 values, columns 8 cg on of this tile's row `row`.
+__device__ __forceinline__ void store_terms(__nv_bfloat16* terms, int row, int cg, int r,
+                                            const float4& a, const float4& b) {
+  const float va[4] = {a.x, a.y, a.z, a.w}, vb[4] = {b.x, b.y, b.z, b.w};
+  uint2 lo[3], hi[3];
+  split4<3>(va, lo);
+  split4<3>(vb, hi);
+#pragma unroll
+  for (int w = 0; w < 3; ++w)
+    *reinterpret_cast<uint4*>(terms + (((size_t)blockIdx.x * kTm + row) * 3 + w) * r + cg * 8) =
+        make_uint4(lo[w].x, lo[w].y, hi[w].x, hi[w].y);
 }
 
 template <bool BWD>
@@ -97,13 +123,13 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* ring = smem + sh.u_bytes;            // u's terms stand first
+  uint8_t* ring = smem;
   uint8_t* aux = ring + sh.stages * sh.stage + kBlk;
   uint64_t* full = reinterpret_cast<uint64_t*>(aux);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* d1_full = empty + kMaxStages;       // [2]
-  uint64_t* d1_empty = d1_full + 2;
-  uint64_t* d2_full = d1_empty + 2;             // [kGroups]
+  uint64_t* d1_full = empty + kMaxStages;
+  uint64_t* d1_empty = d1_full + 1;
+  uint64_t* d2_full = d1_empty + 1;             // [kGroups]
   uint64_t* d2_empty = d2_full + kGroups;
   uint64_t* u_full = d2_empty + kGroups;
   uint64_t* drained = u_full + 1;
@@ -142,10 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
         mbar_init(&empty[s], 1);    // D1: the MMAs' completion; D2: the last epilogue warp
         left[s] = 0;
       }
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&d1_full[b], 1);
-        mbar_init(&d1_empty[b], 4 * kGroups);   // the epilogue warps
-      }
+      mbar_init(d1_full, 1);
+      mbar_init(d1_empty, 4 * kGroups);         // the epilogue warps
       for (int b = 0; b < kGroups; ++b) {
         mbar_init(&d2_full[b], 1);
         mbar_init(&d2_empty[b], 4);             // the group's warps
@@ -162,8 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
   const int nk = ceil_div_dev(K, kKc), nn = ceil_div_dev(N, NC);
-  const int nf = ceil_div_dev(nk, kFlush);
-  const int d1_col = sh.nb * 64, d2_col = 2 * d1_col;   // D1's second buffer, D2's first
+  const int nf = ceil_div_dev(nk, sh.flush);
 
   if (warp == kWeightWarp) {
     // ------------------------------------------------------ weight producer
@@ -250,6 +273,21 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
     constexpr int PU = (kAdapterMaxRank / 8 + 2 * kGroups - 1) / (2 * kGroups);
     const int p0 = warp >> 2;
     const float sc = __ldg(g.scale + a);
+    if (BWD) {
+      // one of the gradient's operands, u's terms, while D1 is formed
+#pragma unroll
+      for (int i = 0; i < PU; ++i) {
+        const int cg = p0 + i * 2 * kGroups;
+        if (cg * 8 >= r) continue;
+        float4 u0 = make_float4(0.f, 0.f, 0.f, 0.f), u1 = u0;
+        if (t >= 0) {
+          const float4* ui = reinterpret_cast<const float4*>(g.u + (size_t)t * r + cg * 8);
+          u0 = __ldg(ui);
+          u1 = __ldg(ui + 1);
+        }
+        store_terms(g.up, row, cg, r, u0, u1);
+      }
+    }
     float acc[PU][8];
 #pragma unroll
     for (int i = 0; i < PU; ++i)
@@ -257,75 +295,59 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     bool alive = true;
     for (int f = 0; f < nf && alive; ++f) {
-      alive = __all_sync(0xffffffffu, mbar_wait(&d1_full[f & 1], (uint32_t)(f >> 1) & 1u));
+      alive = __all_sync(0xffffffffu, mbar_wait(d1_full, (uint32_t)f & 1u));
       if (!alive) break;
       tc_fence_after_sync();
+      uint32_t d[PU][8];
 #pragma unroll
-      for (int i = 0; i < PU; ++i) {
-        const int cg = p0 + i * 2 * kGroups;
-        if (cg * 8 < r) {
-          uint32_t d[8];
-          tmem_ld_32x32b_x8(lanes + (uint32_t)((f & 1) * d1_col + cg * 8), d);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[i][j] += __uint_as_float(d[j]);
-        }
-      }
+      for (int i = 0; i < PU; ++i)
+        if ((p0 + i * 2 * kGroups) * 8 < r)
+          tmem_ld_32x32b_x8(lanes + (uint32_t)(p0 + i * 2 * kGroups) * 8, d[i]);
+      tmem_ld_wait();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d1_empty[f & 1]);
+      if (lane == 0) mbar_arrive(d1_empty);
+#pragma unroll
+      for (int i = 0; i < PU; ++i)
+        if ((p0 + i * 2 * kGroups) * 8 < r)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[i][j] += __uint_as_float(d[i][j]);
     }
 #pragma unroll
     for (int i = 0; i < PU; ++i) {
-      const int cg = p0 + i * 2 * kGroups;   // 8 columns: a 16-byte piece of u's terms
-      if (cg * 8 < r) {
-        uint2 lo[TERMS], hi[TERMS];
-        float v[8];
+      const int cg = p0 + i * 2 * kGroups;   // 8 columns: 4 of tensor memory's a term
+      if (cg * 8 >= sh.rp) continue;         // (columns behind an odd rank: zeros)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = acc[i][j] * sc;
-        const float va[4] = {v[0], v[1], v[2], v[3]}, vb[4] = {v[4], v[5], v[6], v[7]};
-        split4<TERMS>(va, lo);
-        split4<TERMS>(vb, hi);
+      for (int j = 0; j < 8; ++j) acc[i][j] = cg * 8 < r ? acc[i][j] * sc : 0.f;
+      const float va[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+      const float vb[4] = {acc[i][4], acc[i][5], acc[i][6], acc[i][7]};
+      uint2 lo[TERMS], hi[TERMS];
+      split4<TERMS>(va, lo);
+      split4<TERMS>(vb, hi);
 #pragma unroll
-        for (int w = 0; w < TERMS; ++w)
-          *reinterpret_cast<uint4*>(smem + (w * sh.nb + cg / 8) * kBlk + tile_at<8>(row, cg % 8)) =
-              make_uint4(lo[w].x, lo[w].y, hi[w].x, hi[w].y);
-        if (!BWD) {
-          if (t >= 0 && g.u != nullptr) {
-            float4* o = reinterpret_cast<float4*>(g.u + (size_t)t * r + cg * 8);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-          }
-        } else {
-          // the gradient's operands: v's and u's terms
-          float4 u0 = make_float4(0.f, 0.f, 0.f, 0.f), u1 = u0;
-          if (t >= 0) {
-            const float4* ui = reinterpret_cast<const float4*>(g.u + (size_t)t * r + cg * 8);
-            u0 = __ldg(ui);
-            u1 = __ldg(ui + 1);
-          }
-          const float ua[4] = {u0.x, u0.y, u0.z, u0.w}, ub[4] = {u1.x, u1.y, u1.z, u1.w};
-          uint2 ulo[3], uhi[3];
-          split4<3>(ua, ulo);
-          split4<3>(ub, uhi);
-#pragma unroll
-          for (int w = 0; w < TERMS; ++w) {
-            const size_t o = (((size_t)blockIdx.x * kTm + row) * 3 + w) * r + cg * 8;
-            *reinterpret_cast<uint4*>(g.vp + o) = make_uint4(lo[w].x, lo[w].y, hi[w].x, hi[w].y);
-            *reinterpret_cast<uint4*>(g.up + o) =
-                make_uint4(ulo[w].x, ulo[w].y, uhi[w].x, uhi[w].y);
-          }
-        }
-      } else if (cg * 8 < sh.rp) {   // columns behind an odd rank: zeros
-#pragma unroll
-        for (int w = 0; w < TERMS; ++w)
-          *reinterpret_cast<uint4*>(smem + (w * sh.nb + cg / 8) * kBlk + tile_at<8>(row, cg % 8)) =
-              make_uint4(0, 0, 0, 0);
-      }
+      for (int w = 0; w < TERMS; ++w)
+        tmem_st_32x32b_x4(lanes + (uint32_t)(sh.u_col + w * sh.rp / 2 + cg * 4), lo[w].x, lo[w].y,
+                          hi[w].x, hi[w].y);
     }
-    fence_proxy_async_smem();
+    tmem_st_wait();
+    tc_fence_before_sync();
     __syncwarp();
     if (alive && lane == 0) mbar_arrive(u_full);
+    // u, or v's terms, for later launches, while the second product begins
+#pragma unroll
+    for (int i = 0; i < PU; ++i) {
+      const int cg = p0 + i * 2 * kGroups;
+      if (cg * 8 >= r) continue;
+      const float4 v0 = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      const float4 v1 = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+      if (BWD) {
+        store_terms(g.vp, row, cg, r, v0, v1);
+      } else if (t >= 0 && g.u != nullptr) {
+        float4* o = reinterpret_cast<float4*>(g.u + (size_t)t * r + cg * 8);
+        o[0] = v0;
+        o[1] = v1;
+      }
+    }
     // The rows this lane stores: 4 at a time, 8 lanes (128 bytes) each.
     constexpr int HP = BC / 2;   // 16-byte pieces of this half's row
     uint8_t* orow[HP];
@@ -335,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       orow[k] = tt >= 0 ? static_cast<uint8_t*>(g.out) + (size_t)tt * N * OB : nullptr;
     }
     const int ocol = half * (NC / 2) + lane % 8 * PV;   // this lane's first column in a stage
-    const uint32_t acc2 = lanes + (uint32_t)(d2_col + grp * NC + half * (NC / 2));
+    const uint32_t acc2 = lanes + (uint32_t)(sh.d2_col + grp * NC + half * (NC / 2));
     int use = 0;   // stages this group has taken
     for (int i = grp; grp < sh.groups && i < nn && alive; i += sh.groups, ++use) {
       const int slot = (nk + i) % sh.stages;
@@ -394,13 +416,12 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
     auto wait = [](uint64_t* bar, uint32_t ph) {
       return (bool)__all_sync(0xffffffffu, mbar_wait(bar, ph));
     };
-    int slot = 0;
-    uint32_t fph = 0;
+    int slot = 0, in_block = 0;
+    uint32_t fph = 0, d1_ph = 1;
     bool alive = true;
     const uint32_t id1 = idesc(!BWD, sh.rp), id2 = idesc(!BWD, NC);
     for (int s = 0; s < nk && alive; ++s) {
-      const int f = s / kFlush, b = f & 1;
-      if (s % kFlush == 0 && f >= 2) alive = wait(&d1_empty[b], (uint32_t)(f / 2 - 1) & 1u);
+      if (in_block == 0 && s > 0) alive = wait(d1_empty, d1_ph ^= 1u);
       alive = alive && wait(&full[slot], fph);
       if (!alive) break;
       fence_proxy_async_smem();   // the copies' writes, before the tensor core reads them
@@ -408,19 +429,21 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       const uint32_t xs = smem_u32(ring + slot * sh.stage), ws = xs + 2 * kBlk;
 #pragma unroll
       for (int kk = 0; kk < kKc / 16; ++kk)
-        umma_elect(tmem + (uint32_t)(b * d1_col), desc_k(xs + kk / 4 * kBlk + kk % 4 * 32),
+        umma_elect(tmem, desc_k(xs + kk / 4 * kBlk + kk % 4 * 32),
                    BWD ? desc_k(ws + kk / 4 * sh.rp * 128 + kk % 4 * 32)
                        : desc_mn(ws + kk / 4 * sh.nb * kBlk + kk % 4 * 2048, kBlk),
-                   id1, (s % kFlush | kk) != 0 ? 1u : 0u);
+                   id1, (in_block | kk) != 0 ? 1u : 0u);
       umma_commit_elect(&empty[slot]);
-      if (s % kFlush == kFlush - 1 || s == nk - 1) umma_commit_elect(&d1_full[b]);
+      if (++in_block == sh.flush || s == nk - 1) {
+        umma_commit_elect(d1_full);
+        in_block = 0;
+      }
       if (++slot == sh.stages) {
         slot = 0;
         fph ^= 1u;
       }
     }
     alive = alive && wait(u_full, 0);
-    const uint32_t us = smem_u32(smem);
     int b = 0, use = 0;   // output stage i: group b, its use-th
     for (int i = 0; i < nn && alive; ++i) {
       if (use > 0) alive = wait(&d2_empty[b], (uint32_t)(use - 1) & 1u);
@@ -432,11 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       uint32_t more = 0;
       for (int w = TERMS - 1; w >= 0; --w)   // the small terms first
         for (int kk = 0; kk < sh.rp / 16; ++kk) {
-          umma_elect(tmem + (uint32_t)(d2_col + b * NC),
-                       desc_k(us + (w * sh.nb + kk / 4) * kBlk + kk % 4 * 32),
-                       BWD ? desc_k(ws + kk / 4 * kBlk + kk % 4 * 32)
-                           : desc_mn(ws + kk * 2048, sh.rp * 128),
-                       id2, more);
+          umma_elect_ts(tmem + (uint32_t)(sh.d2_col + b * NC),
+                        tmem + (uint32_t)(sh.u_col + w * sh.rp / 2 + kk * 8),
+                        BWD ? desc_k(ws + kk / 4 * kBlk + kk % 4 * 32)
+                            : desc_mn(ws + kk * 2048, sh.rp * 128),
+                        id2, more);
           more = 1;
         }
       umma_commit_elect(&d2_full[b]);
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
 
 template <bool BWD>
 cudaError_t run(const LowRankArgs& g, int tiles, cudaStream_t s) {
-  const TcShape sh = tc_shape<BWD>(g.r);
+  const TcShape sh = tc_shape<BWD>(g.r, BWD || g.u != nullptr);
   const auto kern = low_rank_tc_kernel<BWD>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), 227 * 1024);
   if (e != cudaSuccess) return e;
