@@ -11,8 +11,8 @@
 // product's loads are already in flight, so HBM never waits.  One warp issues
 // the MMAs (M = 128: the upper 64 rows read whatever follows in shared memory,
 // or stands in tensor memory, and are never looked at).  The second product
-// takes u's terms from tensor memory: an MMA of 128 x 64 x 16 whose A is in
-// shared memory takes 49 cycles, 37 of them A's read.  The warps that own
+// takes u's terms from tensor memory: an MMA of 128 x 64 x 16 takes 32 cycles
+// so, 49 with A in shared memory.  The warps that own
 // tensor memory's lanes 0-63 are the epilogue: three groups, an output stage and
 // a D2 buffer each in turn.  They add D1's blocks in round-to-nearest fp32 (the
 // tensor core's own sums truncate), and write D2 through the stage's base tile,
@@ -36,7 +36,7 @@ constexpr int kKc = 128;            // input columns a stage
 // the MMAs, one loads the weights and two idle.
 constexpr int kGroups = 3;
 constexpr int kThreads = 32 * 8 * kGroups;
-constexpr int kProducers = 256;     // threads of the row producers
+constexpr int kProducers = 128;     // threads of the row producers
 constexpr int kMmaWarp = 18, kWeightWarp = 19;
 // Input stages a block of D1's sum: the truncation of 256 columns' sums leaves u
 // and v within 2e-7 of exact, 512's within 4e-7, which u's and v's products, the
@@ -89,7 +89,8 @@ TcShape tc_shape(int r, bool kept) {
   // + kBlk: the MMA's upper rows of the last stage
   t.stages = std::min(kMaxStages, (224 * 1024 - 1024 - kAux - kBlk) / t.stage);
   t.smem = t.stages * t.stage + kBlk + kAux + 1024;
-  // tensor memory: D1, u's terms (two bf16 a column), a D2 for each group
+  // tensor memory: D1, u's terms (two bf16 a column), a D2 for each group; D1's
+  // second buffer is where the D2s come to stand
   t.u_col = t.nb * 64;
   t.d2_col = t.u_col + (BWD ? 3 : 2) * t.rp / 2;
   t.groups = std::min(kGroups, (512 - t.d2_col) / (BWD ? 64 : 128));
@@ -127,9 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   uint8_t* aux = ring + sh.stages * sh.stage + kBlk;
   uint64_t* full = reinterpret_cast<uint64_t*>(aux);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* d1_full = empty + kMaxStages;
-  uint64_t* d1_empty = d1_full + 1;
-  uint64_t* d2_full = d1_empty + 1;             // [kGroups]
+  uint64_t* d1_full = empty + kMaxStages;       // [2]
+  uint64_t* d1_empty = d1_full + 2;
+  uint64_t* d2_full = d1_empty + 2;             // [kGroups]
   uint64_t* d2_empty = d2_full + kGroups;
   uint64_t* u_full = d2_empty + kGroups;
   uint64_t* drained = u_full + 1;
@@ -168,8 +169,10 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
         mbar_init(&empty[s], 1);    // D1: the MMAs' completion; D2: the last epilogue warp
         left[s] = 0;
       }
-      mbar_init(d1_full, 1);
-      mbar_init(d1_empty, 4 * kGroups);         // the epilogue warps
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&d1_full[b], 1);
+        mbar_init(&d1_empty[b], 4 * kGroups);   // the epilogue warps
+      }
       for (int b = 0; b < kGroups; ++b) {
         mbar_init(&d2_full[b], 1);
         mbar_init(&d2_empty[b], 4);             // the group's warps
@@ -218,13 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
         phase ^= 1u;
       }
     }
-  } else if ((warp & 2) != 0 && warp < 2 * kProducers / 32) {
+  } else if ((warp & 3) == 3 && warp < 4 * kProducers / 32) {
     // -------------------------------------------------------- row producers
-    const int p = ((warp >> 2) * 2 + (warp & 1)) * 32 + lane;   // 0 .. kProducers - 1
+    const int p = (warp >> 2) * 32 + lane;   // 0 .. kProducers - 1
     constexpr int R = kTm * 16 / kProducers;   // rows of a thread in a stage, 16 apart
     int tok[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) tok[i] = s_rows[p / 16 + 16 * i];
+    for (int i = 0; i < R; ++i) tok[i] = s_rows[p / 16 + kProducers / 16 * i];
     const int total = nk + nn;
     int slot = 0;
     uint32_t phase = 1;   // of the empty barriers; the first round waits for nothing
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const bool ok = tok[i] >= 0 && col < K;
-          cp_async16(st + (pc >> 3) * kBlk + tile_at<8>(p / 16 + 16 * i, pc & 7),
+          cp_async16(st + (pc >> 3) * kBlk + tile_at<8>(p / 16 + kProducers / 16 * i, pc & 7),
                      ok ? g.in + (size_t)tok[i] * K + col : g.in, ok);
         }
       } else {
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const bool ok = tok[i] >= 0 && col < N && base != nullptr;
-          cp_async16(st + tile_at<BC>(p / 16 + 16 * i, pc),
+          cp_async16(st + tile_at<BC>(p / 16 + kProducers / 16 * i, pc),
                      ok ? base + ((size_t)tok[i] * N + col) * OB
                         : reinterpret_cast<const uint8_t*>(g.in), ok);
         }
@@ -295,18 +298,19 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     bool alive = true;
     for (int f = 0; f < nf && alive; ++f) {
-      alive = __all_sync(0xffffffffu, mbar_wait(d1_full, (uint32_t)f & 1u));
+      alive = __all_sync(0xffffffffu, mbar_wait(&d1_full[f & 1], (uint32_t)(f >> 1) & 1u));
       if (!alive) break;
       tc_fence_after_sync();
+      const uint32_t d1 = lanes + (uint32_t)((f & 1) * sh.d2_col);
       uint32_t d[PU][8];
 #pragma unroll
       for (int i = 0; i < PU; ++i)
         if ((p0 + i * 2 * kGroups) * 8 < r)
-          tmem_ld_32x32b_x8(lanes + (uint32_t)(p0 + i * 2 * kGroups) * 8, d[i]);
+          tmem_ld_32x32b_x8(d1 + (uint32_t)(p0 + i * 2 * kGroups) * 8, d[i]);
       tmem_ld_wait();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(d1_empty);
+      if (lane == 0) mbar_arrive(&d1_empty[f & 1]);
 #pragma unroll
       for (int i = 0; i < PU; ++i)
         if ((p0 + i * 2 * kGroups) * 8 < r)
@@ -416,26 +420,30 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
     auto wait = [](uint64_t* bar, uint32_t ph) {
       return (bool)__all_sync(0xffffffffu, mbar_wait(bar, ph));
     };
-    int slot = 0, in_block = 0;
-    uint32_t fph = 0, d1_ph = 1;
+    int slot = 0, block = 0, in_block = 0;
+    uint32_t fph = 0;
     bool alive = true;
     const uint32_t id1 = idesc(!BWD, sh.rp), id2 = idesc(!BWD, NC);
     for (int s = 0; s < nk && alive; ++s) {
-      if (in_block == 0 && s > 0) alive = wait(d1_empty, d1_ph ^= 1u);
+      if (in_block == 0 && block >= 2)
+        alive = wait(&d1_empty[block & 1], (uint32_t)(block / 2 - 1) & 1u);
       alive = alive && wait(&full[slot], fph);
       if (!alive) break;
       fence_proxy_async_smem();   // the copies' writes, before the tensor core reads them
       tc_fence_after_sync();
       const uint32_t xs = smem_u32(ring + slot * sh.stage), ws = xs + 2 * kBlk;
+      const uint64_t xd = desc_k(xs);
+      const uint64_t wd0 = BWD ? desc_k(ws) : desc_mn(ws, kBlk);
+      const uint64_t wd1 = wd0 + (uint32_t)(BWD ? sh.rp * 128 : sh.nb * kBlk) / 16;
 #pragma unroll
       for (int kk = 0; kk < kKc / 16; ++kk)
-        umma_elect(tmem, desc_k(xs + kk / 4 * kBlk + kk % 4 * 32),
-                   BWD ? desc_k(ws + kk / 4 * sh.rp * 128 + kk % 4 * 32)
-                       : desc_mn(ws + kk / 4 * sh.nb * kBlk + kk % 4 * 2048, kBlk),
-                   id1, (in_block | kk) != 0 ? 1u : 0u);
+        umma_elect(tmem + (uint32_t)((block & 1) * sh.d2_col), xd + (kk / 4 * kBlk + kk % 4 * 32) / 16,
+                   (kk < 4 ? wd0 : wd1) + kk % 4 * (BWD ? 32 : 2048) / 16, id1,
+                   (in_block | kk) != 0 ? 1u : 0u);
       umma_commit_elect(&empty[slot]);
       if (++in_block == sh.flush || s == nk - 1) {
-        umma_commit_elect(d1_full);
+        umma_commit_elect(&d1_full[block & 1]);
+        ++block;
         in_block = 0;
       }
       if (++slot == sh.stages) {
@@ -444,24 +452,33 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       }
     }
     alive = alive && wait(u_full, 0);
+    // (Steps unrolled, their descriptors a constant apart, one election for all:
+    // 40 cycles an MMA of 128 x 64 x 16 where a loop that elects for each took 66.)
+    const int ks = sh.rp / 16;
     int b = 0, use = 0;   // output stage i: group b, its use-th
     for (int i = 0; i < nn && alive; ++i) {
       if (use > 0) alive = wait(&d2_empty[b], (uint32_t)(use - 1) & 1u);
       alive = alive && wait(&full[slot], fph);
       if (!alive) break;
-      fence_proxy_async_smem();
+      // (no proxy fence: these MMAs read tensor memory and the weights' TMA
+      // alone, and the fence waits for the rows' copies in flight)
       tc_fence_after_sync();
       const uint32_t ws = smem_u32(ring + slot * sh.stage) + 2 * kBlk;
-      uint32_t more = 0;
-      for (int w = TERMS - 1; w >= 0; --w)   // the small terms first
-        for (int kk = 0; kk < sh.rp / 16; ++kk) {
-          umma_elect_ts(tmem + (uint32_t)(sh.d2_col + b * NC),
-                        tmem + (uint32_t)(sh.u_col + w * sh.rp / 2 + kk * 8),
-                        BWD ? desc_k(ws + kk / 4 * kBlk + kk % 4 * 32)
-                            : desc_mn(ws + kk * 2048, sh.rp * 128),
-                        id2, more);
-          more = 1;
+      const uint64_t wd = BWD ? desc_k(ws) : desc_mn(ws, sh.rp * 128);
+      const uint32_t d2 = tmem + (uint32_t)(sh.d2_col + b * NC);
+      if (elect_one()) {
+#pragma unroll
+        for (int w = TERMS - 1; w >= 0; --w) {   // the small terms first
+          const uint32_t uw = tmem + (uint32_t)(sh.u_col + w * sh.rp / 2);
+#pragma unroll
+          for (int kk = 0; kk < kAdapterMaxRank / 16; ++kk) {
+            if (kk == ks) break;
+            umma_ts(d2, uw + kk * 8, wd + (BWD ? kk / 4 * kBlk + kk % 4 * 32 : kk * 2048) / 16,
+                    id2, w != TERMS - 1 || kk != 0 ? 1u : 0u);
+          }
         }
+      }
+      __syncwarp();
       umma_commit_elect(&d2_full[b]);
       if (++b == sh.groups) {
         b = 0;
