@@ -821,12 +821,16 @@ int tile_rows(int T, int n) { return T <= 1024 || T <= 32 * n ? 16 : 64; }
 int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
 
 // Whether the low-rank products run on tcgen05, a CTA (and an SM) to a tile of
-// 64 rows: where the tiles give work to more than half of the SMs.  Fewer tiles
-// are shared by clusters of CTAs on mma.sync instead.  Forward and backward on
-// B200, us (tcgen05 against mma.sync): 8192 rows of 2048, rank 64, 113 / 132;
-// of 4096, rank 16, 167 / 186; 6000 of 1024, rank 128, 104 / 126; but 4096 of
-// 2048, rank 64, 99 / 87, and 2048 of 4096 149 / 112.
-bool use_tc(int T, int n) { return tile_rows(T, n) == 64 && T / 64 > device_sm_count() / 2; }
+// 64 rows: where the tiles give work to more than half of the SMs, or a quarter
+// for ranks above 64, whose products weigh more.  Fewer tiles are shared by
+// clusters of CTAs on mma.sync instead.  Forward and backward on B200, us
+// (tcgen05 against mma.sync): 8192 rows of 2048, rank 64, 98 / 132; of 4096, rank
+// 16, 156 / 186; 4096 of 2048, rank 64, 81 / 82; 3200 of 4096, rank 128, 166 /
+// 200; but rank 64, 127 / 124; rank 16, 117 / 91; and 2048 of 2048, rank 128, 95 /
+// 83.
+bool use_tc(int T, int n, int r) {
+  return tile_rows(T, n) == 64 && T / 64 > device_sm_count() / (r > 64 ? 4 : 2);
+}
 
 // Rows by tile slot (the plan's, and u's and v's terms): whole tiles.
 size_t term_rows(int T, int n) { return (size_t)max_tiles(T, n) * tile_rows(T, n); }
@@ -937,7 +941,7 @@ cudaError_t run_grad(const CUtensorMap& mapU, const CUtensorMap& mapV, const Gra
 
 cudaError_t launch_adapter(const AdapterCall& a, bool backward, cudaStream_t s) {
   if (a.c->T == 0) return cudaSuccess;
-  if (use_tc(a.c->T, a.n))
+  if (use_tc(a.c->T, a.n, a.r))
     return launch_low_rank_tc(low_rank_args(a), backward, max_tiles(a.c->T, a.n), s);
   return backward ? run_rank<true>(a, s) : run_rank<false>(a, s);
 }

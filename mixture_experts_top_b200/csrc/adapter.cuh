@@ -97,6 +97,11 @@ __device__ __forceinline__ void umma_elect(uint32_t d_tmem, uint64_t a_desc, uin
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// n of a barrier's counted arrivals.
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+               : "memory");
+}
 // 1 in one lane of a converged warp.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;

