@@ -156,7 +156,9 @@ int moe_combine_dropout_backward(const moe_config_t* cfg, const moe_dropout_t* d
  *   written (0 for one without tokens).  base's gradient is dy.
  *   ws: moe_adapter_workspace_size bytes, 256-byte aligned.
  * Tensor cores with fp32 sums; u and v keep fp32 accuracy as operands (split
- * into bf16 terms).  Fixed orders, no floating-point atomics. */
+ * into bf16 terms: where one is infinite its row, and the gradients of its
+ * adapter, are NaN).  Fixed orders, no floating-point atomics.  Calls on
+ * several streams may share a plan; each needs a workspace of its own. */
 size_t moe_adapter_plan_size(const moe_config_t* cfg, int32_t n_adapters);
 int moe_adapter_plan(const moe_config_t* cfg, int32_t n_adapters, const int32_t* token_adapter,
                      void* plan, size_t plan_bytes, moe_stream_t stream);

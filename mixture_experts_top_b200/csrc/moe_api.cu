@@ -415,8 +415,9 @@ namespace {
 int route_backward_entry(const moe_config_t* cfg, const void* x, const float* W_router,
                          const float* logits, const int32_t* expert_indices, const float* gates,
                          const float* f, const float* dgates, const float* daux, int32_t T_batch,
-                         const float* dlogits_add, float* dx, float* dW_router, float* dbias, float* dlogits, void* ws,
-                         size_t ws_bytes, moe_stream_t stream, const char* name) {
+                         const float* dlogits_add, float* dx, float* dW_router, float* dbias,
+                         float* dlogits, void* ws, size_t ws_bytes, moe_stream_t stream,
+                         const char* name) {
   int st = check_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config_t& c = *cfg;

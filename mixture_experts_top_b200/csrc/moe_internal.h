@@ -306,7 +306,7 @@ constexpr int kAdapterMaxCount = 1024;
 constexpr int kAdapterMaxRank = 128;
 struct AdapterPlanLayout {
   size_t ctrl;      // error word (256 bytes, the header in them)
-  size_t header;    // int32: T, n, tiles
+  size_t header;    // int32: T, n
   size_t offsets;   // (n + 2) int32: rows of adapter a; group n: no adapter
   size_t rows;      // int32: tokens by group, in token order, by tile slot (-1: none)
   size_t tiles;     // int2: group, rows

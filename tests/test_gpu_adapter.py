@@ -95,7 +95,7 @@ def _check(i, got, base=True, dx_add=True):
     # many rows: the tcgen05 products
     (4800, 64, 64, 1, 16), (4801, 72, 40, 40, 8), (4900, 776, 1032, 5, 24), (5000, 520, 264, 7, 32),
     (5200, 1032, 200, 3, 64), (6000, 136, 648, 3, 128), (4999, 2056, 72, 2, 72),
-    (8192, 200, 136, 6, 88), (20000, 40, 24, 2, 8)])
+    (8192, 200, 136, 6, 88), (20000, 40, 24, 2, 8), (3000, 264, 136, 2, 96)])
 def test_sizes(T, d, d_out, n, r):
     i = _inputs(T, d, d_out, n, r, seed=T + r)
     _check(i, _run(i, T, d, d_out, n, r))
@@ -286,3 +286,29 @@ def test_two_layers_share_a_plan():
         api.moe_adapter(cfg, plan, q["x"], q["A"], q["B"], q["scale"], q["base"], out, None)
         ref = _run({**q, "ids": i["ids"]}, T, 64, 136, n, q["A"].shape[2])[0]
         assert torch.equal(out, ref)
+
+
+def test_two_streams_share_a_plan():
+    """Two layers' backwards at once, each with its own workspace."""
+    T, d, w, n, r = 5000, 264, 136, 3, 32
+    ins = [_inputs(T, d, w, n, r, seed=s) for s in (13, 14)]
+    ins[1]["ids"] = ins[0]["ids"]
+    cfg = _cfg(T, d, w)
+    plan = _plan(cfg, n, ins[0]["ids"])
+    want = [_run(i, T, d, w, n, r) for i in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    e = lambda *s: torch.empty(s, device="cuda")
+    bufs = [(torch.empty_like(i["base"]), torch.full((T, r), float("nan"), device="cuda"), e(T, d),
+             e(n, d, r), e(n, r, w), api.alloc_adapter_workspace(cfg, n, r)) for i in ins]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, s, (out, u, dx, dA, dB, ws) in zip(ins, streams, bufs):
+            with torch.cuda.stream(s):
+                api.moe_adapter(cfg, plan, i["x"], i["A"], i["B"], i["scale"], i["base"], out, u)
+                api.moe_adapter_backward(cfg, plan, i["x"], u, i["dy"], i["A"], i["B"],
+                                         i["scale"], i["dx_add"], dx, dA, dB, ws)
+    torch.cuda.synchronize()
+    assert api.moe_device_status(plan) == 0
+    for b, q in zip(bufs, want):
+        for x, y in zip(b[:5], q):
+            assert torch.equal(x.nan_to_num(7), y.nan_to_num(7))
