@@ -94,16 +94,18 @@ struct Lanes {
   }
 };
 
-// This lane's logits of token t; -inf where there is none.
+// This lane's logits of token t, -inf beyond the last expert; a token that is not
+// in is not read: zeros, whose softmax is finite.
 template <typename L>
 __device__ __forceinline__ void load_logits(const float* __restrict__ logits, int t, bool in,
                                             int E, int gl, float (&v)[L::NV]) {
   const float* row = logits + (size_t)t * E;
+  const float fill = in ? -INFINITY : 0.f;
   if constexpr (L::VEC) {
 #pragma unroll
     for (int i = 0; i < L::NV; i += 4) {
       const int e = L::expert(gl, i);
-      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      float4 q = make_float4(fill, fill, fill, fill);
       if (in && e < E) q = __ldg(reinterpret_cast<const float4*>(row + e));
       v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
     }
@@ -111,7 +113,7 @@ __device__ __forceinline__ void load_logits(const float* __restrict__ logits, in
 #pragma unroll
     for (int i = 0; i < L::NV; ++i) {
       const int e = L::expert(gl, i);
-      v[i] = in && e < E ? __ldg(row + e) : -INFINITY;
+      v[i] = in && e < E ? __ldg(row + e) : fill;
     }
   }
 }
@@ -135,22 +137,18 @@ __device__ __forceinline__ void store_values(float* row, int E, int gl, const fl
   }
 }
 
-// exp(d) for d <= 0 as 2^(d log2 e): one product and the hardware's 2^x, within
-// 2.3 |d| + 4 half steps of fp32.  With expf, whose exact range reduction is six
-// more instructions a logit, instructions and not HBM bound these kernels: the
-// forward's first launch took 57 us, against 44, at 131072 x 256.
-__device__ __forceinline__ float exp_neg(float d) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.44269504f));
-  return r;
-}
-
 // exp(l - max) of this lane's experts, their sum's inverse and the token's
-// log-sum-exp, from the G lanes' logits; all 0 where act is false (the logits
-// may then hold anything).
+// log-sum-exp, from the G lanes' logits.  Where act is false they are zeros, and
+// so are inv and lse.
+// exp(d), d = l - m <= 0, is 2^(d log2 e): one product and the hardware's 2^x,
+// within 2.3 |d| + 4 half steps of fp32.  (One fused 2^(l log2e - m log2e) would
+// overflow for logits at the type's lowest value.)  With expf, whose exact range
+// reduction is six more instructions a logit, the forward's first launch took 57
+// us, against 44, at 131072 x 256.
 template <typename L>
 __device__ __forceinline__ void softmax_terms(float (&v)[L::NV], bool act, float& inv,
                                               float& lse) {
+  constexpr float kLog2e = 1.44269504f;
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < L::NV; ++i) m = fmaxf(m, v[i]);
@@ -158,8 +156,7 @@ __device__ __forceinline__ void softmax_terms(float (&v)[L::NV], bool act, float
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < L::NV; ++i) {
-    const float ex = exp_neg(v[i] - m);
-    v[i] = act ? ex : 0.f;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[i]) : "f"((v[i] - m) * kLog2e));
     sum += v[i];
   }
   sum = group_sum<L::G>(sum);
@@ -240,13 +237,8 @@ __device__ void finish_sequence(FinishSmem<NT>& sm, const BalanceParts& part,
   const int ni = slots.count();
   double p = 0.0, z = 0.0;
   int c = 0, n = 0;
-  for (int i = tid; i < ni; i += NT) {
-    const size_t at = slots(i);
-    n += __ldcg(part.n + at);
-    z += (double)__ldcg(part.z + at);
-  }
   if (e < E) {
-    constexpr int U = 8;   // slots in flight
+    constexpr int U = 16;   // slots in flight
     for (int i = gi; i < ni; i += U * ng) {
       float pv[U];
       int cv[U];
@@ -263,6 +255,11 @@ __device__ void finish_sequence(FinishSmem<NT>& sm, const BalanceParts& part,
         c += cv[u];
       }
     }
+  }
+  for (int i = tid; i < ni; i += NT) {
+    const size_t at = slots(i);
+    n += __ldcg(part.n + at);
+    z += (double)__ldcg(part.z + at);
   }
   n = __reduce_add_sync(0xffffffffu, n);
   z = warp_sum(z);
@@ -390,6 +387,9 @@ __global__ void __launch_bounds__(256, 4)
   if (lane == 0) first_seq[warp] = s;
   __syncthreads();
   const int s0 = first_seq[0];
+  auto counted = [&](int t, int end) {
+    return t < end && (mask == nullptr || __ldg(mask + t) != 0);
+  };
   bool merged = false;   // one sequence holds the whole CTA's tokens
   if (s0 < S) {
     seq_bounds(off, s0, T, lo, hi);
@@ -403,7 +403,11 @@ __global__ void __launch_bounds__(256, 4)
     const int b = max(lo, t0), e1 = min(hi, t1);
     if (!merged && b >= e1) continue;
     if (b != t0) load_logits<L>(logits, b + g, b + g < e1, E, gl, nxt);
-    bool nact = b + g < e1 && (mask == nullptr || __ldg(mask + b + g) != 0);
+    bool nact = counted(b + g, e1), nact2 = counted(b + W + g, e1);
+    if (!nact) {   // read ahead: may hold anything
+#pragma unroll
+      for (int i = 0; i < NV; ++i) nxt[i] = 0.f;
+    }
     for (int e = lane; e < E; e += 32) hist[warp][e] = 0;
     __syncwarp();
     for (int i0 = b * k + lane; i0 < e1 * k; i0 += 128) {
@@ -432,9 +436,9 @@ __global__ void __launch_bounds__(256, 4)
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = nxt[i];
       const bool act = nact;
-      const int tn = tb + W + g;
-      nact = tn < e1 && (mask == nullptr || __ldg(mask + tn) != 0);
-      load_logits<L>(logits, tn, tn < e1, E, gl, nxt);
+      nact = nact2;
+      load_logits<L>(logits, tb + W + g, nact, E, gl, nxt);
+      nact2 = counted(tb + 2 * W + g, e1);
       softmax_terms<L>(v, act, inv, lse);
 #pragma unroll
       for (int i = 0; i < NV; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
@@ -536,6 +540,9 @@ __global__ void __launch_bounds__(256, 4)
   const int N = __ldg(tokens + S), live = __ldg(tokens + S + 1);
   const float dz = N > 0 ? (float)(2.0 * (double)__ldg(dlosses + 1) / (double)N) : 0.f;
   const double db = live > 0 ? (double)__ldg(dlosses) * E / (double)live : 0.0;
+  auto counted = [&](int t, int end) {
+    return t < end && (mask == nullptr || __ldg(mask + t) != 0);
+  };
   auto zero_rows = [&](int b, int e) {
     for (size_t i = (size_t)b * E + lane; i < (size_t)e * E; i += 32) dlogits[i] = 0.f;
   };
@@ -560,26 +567,29 @@ __global__ void __launch_bounds__(256, 4)
       const int e = L::expert(gl, i);
       a[i] = e < E ? (float)(w * (double)__ldg(counts + (size_t)s * E + e)) : 0.f;
     }
-    bool nact = b + g < e1 && (mask == nullptr || __ldg(mask + b + g) != 0);
     if (b != t0) load_logits<L>(logits, b + g, b + g < e1, E, gl, nxt);
+    bool nact = counted(b + g, e1), nact2 = counted(b + W + g, e1);
+    if (!nact) {   // read ahead: may hold anything
+#pragma unroll
+      for (int i = 0; i < NV; ++i) nxt[i] = 0.f;
+    }
     for (int tb = b; tb < e1; tb += W) {
       float v[NV], inv, lse;
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = nxt[i];
       const bool act = nact;
-      const int t = tb + g, tn = t + W;
-      nact = tn < e1 && (mask == nullptr || __ldg(mask + tn) != 0);
-      load_logits<L>(logits, tn, tn < e1, E, gl, nxt);
+      const int t = tb + g;
+      nact = nact2;
+      load_logits<L>(logits, t + W, nact, E, gl, nxt);
+      nact2 = counted(t + 2 * W, e1);
       softmax_terms<L>(v, act, inv, lse);
       float pa = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        v[i] *= inv;
-        pa = fmaf(v[i], a[i], pa);
-      }
-      pa = dz * lse - group_sum<G>(pa);
+      for (int i = 0; i < NV; ++i) pa = fmaf(v[i], a[i], pa);
+      pa = dz * lse - inv * group_sum<G>(pa);
+      pa *= inv;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = act ? v[i] * (a[i] + pa) : 0.f;
+      for (int i = 0; i < NV; ++i) v[i] = act ? v[i] * fmaf(a[i], inv, pa) : 0.f;
       if (t < e1) store_values<L>(dlogits + (size_t)t * E, E, gl, v);
     }
   }

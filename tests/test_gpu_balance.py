@@ -155,6 +155,25 @@ def test_experts_switched_off():
     assert (P[:, 5] == 0).all() and (g[:, 5] == 0).all()
 
 
+@pytest.mark.parametrize("E", [8, 64, 100, 256])
+def test_logits_at_the_lowest_value(E):
+    """Experts switched off by the type's lowest value instead of -inf, up to all
+    of a token's: P stays a distribution, and without the z-loss's weight the
+    gradient is finite."""
+    T, k, low = 70, 2, np.finfo(np.float32).min
+    rng, L, idx = _case(T, E, k, 12)
+    L[rng.random((T, E)) < 0.5] = low
+    L[[3, 40]] = low
+    c, P, n, loss, g, ws = _run(L, idx, E, None, None, np.array([0.7, 0.0], np.float32))
+    r = Q.balance_loss(L, idx, E, None, None)
+    assert np.array_equal(c, r["counts"]) and np.array_equal(n, r["tokens"])
+    assert np.all(np.abs(P - r["prob_mean"]) <= 160 * U * r["prob_mean"])
+    assert abs(loss[0] - r["balance"]) <= 200 * U * r["balance"]
+    ref = Q.balance_loss_backward(L, idx, E, None, None, float(np.float32(0.7)), 0.0)
+    a = 0.7 * E / T * r["counts"][0] / (T * k)
+    assert np.all(np.abs(g - ref) <= 160 * U * 2 * a.max() + 1e-37)
+
+
 def test_no_tokens():
     cfg = _cfg(0, 4, 2)
     ws = api.alloc_balance_workspace(cfg, 2)
