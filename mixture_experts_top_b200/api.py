@@ -408,11 +408,15 @@ def _opt(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
-def _device() -> int:
-    """The current device, which the call's tensors must be on (-2, no
-    tensor's device, before CUDA is initialised)."""
+def _where(stream):
+    """The current device, which the call's tensors must be on (-2, no tensor's
+    device, before CUDA is initialised), and the stream's handle."""
     import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    if not torch.cuda.is_initialized():
+        return -2, None
+    dev = torch._C._cuda_getDevice()
+    return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                 else stream.cuda_stream)
 
 
 def _act(cfg):
@@ -459,7 +463,7 @@ def moe_balance_loss(cfg, seq_offsets, token_mask, logits, expert_indices, count
     token_mask (T) uint8 or None; see include/moe_packed.h for the outputs."""
     import torch
     f32, i32 = torch.float32, torch.int32
-    dev = _device()
+    dev, st = _where(stream)
     n, off = _seqs(seq_offsets, i32, dev)
     T, E = cfg.T, cfg.E
     wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
@@ -469,14 +473,14 @@ def moe_balance_loss(cfg, seq_offsets, token_mask, logits, expert_indices, count
         _arg(expert_indices, "expert_indices", i32, (T, cfg.top_k), dev),
         _arg(counts, "counts", i32, (n, E), dev), _arg(prob_mean, "prob_mean", f32, (n, E), dev),
         _arg(tokens, "tokens", i32, (n + 2,), dev), _arg(losses, "losses", f32, (2,), dev), wp, wn,
-        _stream(stream)), "moe_balance_loss")
+        st), "moe_balance_loss")
 
 
 def moe_balance_loss_backward(cfg, seq_offsets, token_mask, logits, counts, tokens, dlosses,
                               dlogits, ws, stream=None) -> None:
     import torch
     f32, i32 = torch.float32, torch.int32
-    dev = _device()
+    dev, st = _where(stream)
     n, off = _seqs(seq_offsets, i32, dev)
     T, E = cfg.T, cfg.E
     wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
@@ -484,7 +488,7 @@ def moe_balance_loss_backward(cfg, seq_offsets, token_mask, logits, counts, toke
         ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,), dev),
         _arg(logits, "logits", f32, (T, E), dev), _arg(counts, "counts", i32, (n, E), dev),
         _arg(tokens, "tokens", i32, (n + 2,), dev), _arg(dlosses, "dlosses", f32, (2,), dev),
-        _arg(dlogits, "dlogits", f32, (T, E), dev), wp, wn, _stream(stream)),
+        _arg(dlogits, "dlogits", f32, (T, E), dev), wp, wn, st),
         "moe_balance_loss_backward")
 
 
@@ -493,12 +497,12 @@ def moe_route_backward_add(cfg, x, W_router, logits, expert_indices, gates, f, d
                            stream=None) -> None:
     """moe_route_backward with dlogits_add (T, E) fp32 added to the logits' gradient."""
     import torch
-    dev = _device()
+    dev, st = _where(stream)
     add = _arg(dlogits_add, "dlogits_add", torch.float32, (cfg.T, cfg.E), dev)
     _check(load_library().moe_route_backward_add(
         ctypes.byref(cfg), _ptr(x), _ptr(W_router), _ptr(logits), _ptr(expert_indices),
         _ptr(gates), _ptr(f), _ptr(dgates), _ptr(daux), int(T_batch), add, _ptr(dx),
-        _ptr(dW_router), _ptr(dbias), _ptr(dlogits), _ptr(ws), ws.numel(), _stream(stream)),
+        _ptr(dW_router), _ptr(dbias), _ptr(dlogits), _ptr(ws), ws.numel(), st),
         "moe_route_backward_add")
 
 
@@ -520,12 +524,12 @@ def moe_dropout(cfg, p, seed, offset, token_base, x, add, out, stream=None) -> N
         raise ValueError(f"x must be bfloat16 or float32, got {dt}")
     if len(shape) != 2 or shape[0] != cfg.T:
         raise ValueError(f"x must have shape ({cfg.T}, width), got {tuple(shape)}")
-    dev = _device()
+    dev, st = _where(stream)
     d = _drop(p, seed, offset, token_base, dev)
     _check(load_library().moe_dropout(
         ctypes.byref(cfg), ctypes.byref(d), shape[1],
         DTYPES["bf16"] if dt is torch.bfloat16 else DTYPES["f32"], _arg(x, "x", dt, None, dev),
-        _opt(add, "add", dt, shape, dev), _arg(out, "out", dt, shape, dev), _stream(stream)),
+        _opt(add, "add", dt, shape, dev), _arg(out, "out", dt, shape, dev), st),
         "moe_dropout")
 
 
@@ -534,26 +538,26 @@ def moe_combine_dropout(cfg, p, seed, offset, token_base, y_perm, dest, gates, r
     """moe_combine with dropout, plus residual (or None) added after it."""
     import torch
     f32, act, T, k, w = torch.float32, _act(cfg), cfg.T, cfg.top_k, cfg.d_out
-    dev = _device()
+    dev, st = _where(stream)
     d = _drop(p, seed, offset, token_base, dev)
     _check(load_library().moe_combine_dropout(
         ctypes.byref(cfg), ctypes.byref(d), _arg(y_perm, "y_perm", f32, (T * k, w), dev),
         _arg(dest, "dest", torch.int32, (T, k), dev), _arg(gates, "gates", f32, (T, k), dev),
         _opt(residual, "residual", act, (T, w), dev), _arg(output, "output", act, (T, w), dev),
-        _stream(stream)), "moe_combine_dropout")
+        st), "moe_combine_dropout")
 
 
 def moe_combine_dropout_backward(cfg, p, seed, offset, token_base, dy, y_perm, dest, gates,
                                  dy_perm, dgates, stream=None) -> None:
     import torch
     f32, act, T, k, w = torch.float32, _act(cfg), cfg.T, cfg.top_k, cfg.d_out
-    dev = _device()
+    dev, st = _where(stream)
     d = _drop(p, seed, offset, token_base, dev)
     _check(load_library().moe_combine_dropout_backward(
         ctypes.byref(cfg), ctypes.byref(d), _arg(dy, "dy", act, (T, w), dev),
         _arg(y_perm, "y_perm", f32, (T * k, w), dev), _arg(dest, "dest", torch.int32, (T, k), dev),
         _arg(gates, "gates", f32, (T, k), dev), _arg(dy_perm, "dy_perm", f32, (T * k, w), dev),
-        _arg(dgates, "dgates", f32, (T, k), dev), _stream(stream)), "moe_combine_dropout_backward")
+        _arg(dgates, "dgates", f32, (T, k), dev), st), "moe_combine_dropout_backward")
 
 
 def moe_adapter_plan_size(cfg: MoeConfig, n_adapters: int) -> int:
@@ -582,11 +586,11 @@ def alloc_adapter_workspace(cfg: MoeConfig, n_adapters: int, rank: int, device="
 def moe_adapter_plan(cfg, n_adapters, token_adapter, plan, stream=None) -> None:
     """Groups the tokens by adapter: token_adapter (T) int32, negative for none."""
     import torch
-    dev = _device()
+    dev, st = _where(stream)
     pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
     _check(load_library().moe_adapter_plan(
         ctypes.byref(cfg), int(n_adapters),
-        _arg(token_adapter, "token_adapter", torch.int32, (cfg.T,), dev), pp, pn, _stream(stream)),
+        _arg(token_adapter, "token_adapter", torch.int32, (cfg.T,), dev), pp, pn, st),
         "moe_adapter_plan")
 
 
@@ -601,14 +605,14 @@ def moe_adapter(cfg, plan, x, A, B, scale, base, output, u, stream=None) -> None
     import torch
     bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
     n, r = _adapter_shape(cfg, A)
-    dev = _device()
+    dev, st = _where(stream)
     pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
     _check(load_library().moe_adapter(
         ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d), dev),
         _arg(A, "A", bf, None, dev),
         _arg(B, "B", bf, (n, r, w), dev), _arg(scale, "scale", f32, (n,), dev),
         _opt(base, "base", bf, (T, w), dev), _arg(output, "output", bf, (T, w), dev),
-        _opt(u, "u", f32, (T, r), dev), _stream(stream)), "moe_adapter")
+        _opt(u, "u", f32, (T, r), dev), st), "moe_adapter")
 
 
 def moe_adapter_backward(cfg, plan, x, u, dy, A, B, scale, dx_add, dx, dA, dB, ws,
@@ -616,7 +620,7 @@ def moe_adapter_backward(cfg, plan, x, u, dy, A, B, scale, dx_add, dx, dA, dB, w
     import torch
     bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
     n, r = _adapter_shape(cfg, A)
-    dev = _device()
+    dev, st = _where(stream)
     pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
     wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
     _check(load_library().moe_adapter_backward(
@@ -626,4 +630,4 @@ def moe_adapter_backward(cfg, plan, x, u, dy, A, B, scale, dx_add, dx, dA, dB, w
         _arg(B, "B", bf, (n, r, w), dev),
         _arg(scale, "scale", f32, (n,), dev), _opt(dx_add, "dx_add", f32, (T, cfg.d), dev),
         _arg(dx, "dx", f32, (T, cfg.d), dev), _arg(dA, "dA", f32, A.shape, dev),
-        _arg(dB, "dB", f32, (n, r, w), dev), wp, wn, _stream(stream)), "moe_adapter_backward")
+        _arg(dB, "dB", f32, (n, r, w), dev), wp, wn, st), "moe_adapter_backward")
