@@ -821,28 +821,34 @@ __global__ void __launch_bounds__(256) adapter_reduce_kernel(GradArgs g) {
 int rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
 // Rows of a tile: 16 where there are few rows, in all or an adapter (decode),
-// so that they spread over the SMs and a tile is not mostly padding.
+// so that they spread over the SMs and a tile is not mostly padding.  Forward and
+// backward on B200, 2048 columns, us (16 against 64 rows): 1000 rows on 4
+// adapters, rank 64, 47 / 52; 2000 on 100, rank 16, 75 / 87; but 1500 on 4, rank
+// 64, 67 / 57, and 4000 on 100, rank 64, 180 / 145.
 int tile_rows(int T, int n) { return T <= 1024 || T <= 32 * n ? 16 : 64; }
 
 int max_tiles(int T, int n) { return T / tile_rows(T, n) + n + 1; }
 
 // Whether the low-rank products run on tcgen05, a CTA (and an SM) to a tile of
-// 64 rows: where the tiles give work to more than half of the SMs, or a quarter
-// for ranks above 64, whose products weigh more.  Fewer tiles are shared by
-// clusters of CTAs on mma.sync instead.  Forward and backward on B200, us
-// (tcgen05 against mma.sync): 8192 rows of 2048, rank 64, 98 / 132; of 4096, rank
-// 16, 156 / 186; 4096 of 2048, rank 64, 81 / 82; 3200 of 4096, rank 128, 166 /
-// 200; but rank 64, 127 / 124; rank 16, 117 / 91; and 2048 of 2048, rank 128, 95 /
-// 83.
+// 64 rows, by the tiles (each adapter's last one in part): where they give work to
+// more than half of the SMs; a quarter for ranks above 64, whose products weigh
+// more, two thirds up to rank 16.  Fewer tiles are shared by clusters of CTAs on
+// mma.sync instead.  Forward and backward on B200, 2048 columns, us (tcgen05
+// against mma.sync): 8192 rows on 8 adapters, rank 64, 98 / 132; 4000 on 100, 145
+// / 242; 4500 on 4, 83 / 112, but 3200 on 12, 83.4 / 82.7; rank 16: 6600 on 6, 86 /
+// 93, but 5800 on 6, 81 / 75; rank 128, 4096 columns: 3200 on 8, 166 / 200.
 bool use_tc(int T, int n, int r) {
-  return tile_rows(T, n) == 64 && T / 64 > device_sm_count() / (r > 64 ? 4 : 2);
+  const int tiles = T / 64 + n, sms = device_sm_count();
+  return tile_rows(T, n) == 64 && tiles > (r > 64 ? sms / 4 : r > 16 ? sms / 2 : sms * 2 / 3);
 }
 
 // Rows by tile slot (the plan's, and u's and v's terms): whole tiles.
 size_t term_rows(int T, int n) { return (size_t)max_tiles(T, n) * tile_rows(T, n); }
 
 // Chunks of the gradient's rows: two CTAs an SM, but 256 rows at least (a part's
-// trip through memory costs more) and kGradMax at most.
+// trip through memory costs more) and kGradMax at most.  With 128 at least, 1000
+// rows of 2048, rank 64, took 49 us forward and backward against 47; with 512, 64
+// rows on 64 adapters of 4096, rank 16, 59 against 53.
 int grad_chunks(const moe_config_t& c, int n) {
   const int mb = ceil_div(c.d, kGradCols) + ceil_div(c.d_out, kGradCols);
   const int64_t rows = (int64_t)term_rows(c.T, n);
@@ -901,7 +907,8 @@ LowRankArgs low_rank_args(const AdapterCall& a) {
 template <int RP, int TM, bool BWD>
 cudaError_t run_low_rank(const AdapterCall& a, cudaStream_t s) {
   using L = LowRank<RP, TM, BWD>;
-  // CTAs of a tile's cluster: as many as the SMs hold at a time
+  // CTAs of a tile's cluster: as many as the SMs hold at a time.  (Past that a
+  // second wave starts: 4500 rows take 112 us where 4096 take 82.)
   const int tiles = max_tiles(a.c->T, a.n);
   const int most = std::min(ceil_div(a.K, L::KC), ceil_div(a.N, L::NC));
   const int64_t room = (int64_t)std::min(L::CTAS, 4) * device_sm_count();

@@ -13,8 +13,10 @@
 //             a_se = dbalance E f[s,e] / (S+ n_s)
 //   (f counts slots and carries no gradient; rows not counted get 0)
 //
-// Both directions are one pass over the logits: bound by HBM for large T x E,
-// by launch latency below about a million logits.  A token's E logits sit in
+// Both directions are one pass over the logits: bound by HBM for large T x E
+// (B200, 131072 x 256: first launch 34 us, 4.1 TB/s, where load latency and issue
+// slots count too; second 13; backward 46, 5.9 TB/s), by launch latency below
+// about a million logits.  A token's E logits sit in
 // the registers of G <= 16 lanes (32 where they cannot be read by 16-byte
 // vectors), so a warp works on 32 / G tokens at once; maximum and sum are
 // butterflies over the G lanes, in fp32.
@@ -358,7 +360,8 @@ __device__ __forceinline__ bool last_cta(unsigned* done) {
 }
 
 // FUSED: the last CTA also adds up the sequences (few CTAs and sequences:
-// the second launch would cost more than its work).
+// the second launch would cost more than its work; 64 x 8 in both directions: 11.6
+// us against 14.0).
 template <typename L, bool FUSED>
 __global__ void __launch_bounds__(256, 4)
     balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
@@ -510,6 +513,8 @@ __global__ void __launch_bounds__(256, 4)
 // One CTA per sequence (strided); the last CTA to finish adds the sequences.
 // NT threads: 1024 where the sequences are fewer than the SMs (and so may be
 // long, with a slot for every 64 tokens or more), else 256, several CTAs an SM.
+// Both directions: 22002 x 256, 7 sequences, 40 us with 1024 and 64 with 256;
+// 131072 x 256, 311 sequences, 100 and 96.
 template <int NT>
 __global__ void __launch_bounds__(NT)
     balance_finish_kernel(BalanceParts part, const int32_t* __restrict__ off, int T, int E, int k,
@@ -596,7 +601,8 @@ __global__ void __launch_bounds__(256, 4)
 }
 
 // log2 of a warp's tokens C: the fewest (8, 16, ...) that give at most 32
-// warps to each of 148 SMs.
+// warps to each of 148 SMs.  Both directions at 131072 x 256, 311 sequences: 96
+// us; with half the tokens a warp 99, with twice as many 107.
 int chunk_log(int T) {
   int lc = 3;
   while ((T >> lc) >= 148 * 32 && lc < 20) ++lc;
@@ -605,7 +611,8 @@ int chunk_log(int T) {
 
 // Calls f with the lane layout for E experts; vec: E a multiple of 4 and every
 // row of fp32 values 16-byte aligned.  At most 16 values a lane, so that a
-// token's, the next one's and the sums stay in registers.
+// token's, the next one's and the sums stay in registers (E = 256 by 32 lanes of
+// 8: the forward's first launch takes 40 us against 36 at 131072 tokens).
 template <typename F>
 cudaError_t by_width(int E, bool vec, F&& f) {
   if (vec) {

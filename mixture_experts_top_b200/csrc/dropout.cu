@@ -23,7 +23,8 @@ namespace moe {
 namespace {
 
 // Block b of 8 elements: thread-strided, U blocks a thread with all their
-// loads issued first.
+// loads issued first.  At 8192 x 4096 fp32 with an addend 403 MB in 59 us, the
+// measured copy rate and a little more.
 template <typename T, int U, bool ADD>
 __global__ void __launch_bounds__(256)
     dropout_kernel(const T* x, const T* add, T* out, long long nblk, DropArgs d) {
@@ -62,7 +63,8 @@ __global__ void __launch_bounds__(256)
 // longer at top-6).  At 8192 x 4096 top-2 the forward moves its 402 MB in 68 us
 // and the backward its 604 MB in 94 (0.90 and 0.98 of the measured copy rate);
 // at 5003 x 2056 top-6 with 43% of the slots kept, 147 MB in 35 us and 232 MB in
-// 56 (0.64 each): few rows a token are in flight there.
+// 56 (0.64 each): few rows a token are in flight there (both directions 93 us;
+// with one warp a token 95, four 98, eight 114).
 
 // The kept slots of token t in order (nk of them, the same in every lane):
 // their grouped rows and gates; lane i < nk holds its slot's number in `slot`.

@@ -95,20 +95,21 @@ def _check(i, got, base=True, dx_add=True):
     # many rows: the tcgen05 products
     (4800, 64, 64, 1, 16), (4801, 72, 40, 40, 8), (4900, 776, 1032, 5, 24), (5000, 520, 264, 7, 32),
     (5200, 1032, 200, 3, 64), (6000, 136, 648, 3, 128), (4999, 2056, 72, 2, 72),
-    (8192, 200, 136, 6, 88), (20000, 40, 24, 2, 8), (3000, 264, 136, 2, 96)])
+    (8192, 200, 136, 6, 88), (20000, 40, 24, 2, 8), (3000, 264, 136, 2, 96),
+    (6600, 776, 264, 5, 16), (4000, 136, 72, 100, 64)])
 def test_sizes(T, d, d_out, n, r):
     i = _inputs(T, d, d_out, n, r, seed=T + r)
     _check(i, _run(i, T, d, d_out, n, r))
 
 
-@pytest.mark.parametrize("T", [40, 1500, 4800])
+@pytest.mark.parametrize("T", [40, 1500, 4800, 6600])
 @pytest.mark.parametrize("base,dx_add", [(False, True), (True, False), (False, False)])
 def test_without_addends(T, base, dx_add):
     i = _inputs(T, 136, 264, 3, 16, seed=1)
     _check(i, _run(i, T, 136, 264, 3, 16, base, dx_add), base, dx_add)
 
 
-@pytest.mark.parametrize("T", [50, 1500, 4900])
+@pytest.mark.parametrize("T", [50, 1500, 4900, 6600])
 @pytest.mark.parametrize("ids", ["none", "one", "last"])
 def test_extreme_groups(T, ids):
     """No token with an adapter; all on one; only the last token on the last."""
@@ -122,7 +123,7 @@ def test_extreme_groups(T, ids):
     assert (got[3][idle] == 0).all() and (got[4][idle] == 0).all()
 
 
-@pytest.mark.parametrize("T", [300, 4800])
+@pytest.mark.parametrize("T", [300, 4800, 6600])
 def test_in_place(T):
     d, w, n, r = 136, 264, 4, 16
     i = _inputs(T, d, w, n, r, seed=3)
@@ -137,7 +138,7 @@ def test_in_place(T):
     assert torch.equal(y, out) and torch.equal(g, dx)
 
 
-@pytest.mark.parametrize("T", [200, 1400, 4900])
+@pytest.mark.parametrize("T", [200, 1400, 4900, 6600])
 def test_rows_do_not_leak_into_one_another(T):
     """NaN in the rows of one adapter and of tokens without one stays there."""
     d, w, n, r = 72, 136, 3, 16
