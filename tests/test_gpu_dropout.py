@@ -145,7 +145,9 @@ def _combine_case(T, d_out, E, k, dtype, cf, seed):
 
 @pytest.mark.parametrize("T,d_out,E,k,dtype,cf", [
     (1, 8, 2, 1, "bf16", 0.0), (65, 264, 8, 2, "bf16", 0.0), (200, 768, 16, 1, "bf16", 0.5),
-    (77, 1032, 16, 6, "bf16", 0.4), (64, 32, 8, 2, "f32", 0.0), (130, 520, 8, 8, "f32", 0.7)])
+    (77, 1032, 16, 6, "bf16", 0.4), (64, 32, 8, 2, "f32", 0.0), (130, 520, 8, 8, "f32", 0.7),
+    (33, 2056, 64, 6, "bf16", 0.3), (17, 4104, 16, 8, "f32", 0.0), (9, 8200, 8, 5, "bf16", 0.2),
+    (50, 1536, 8, 4, "bf16", 0.5)])
 @pytest.mark.parametrize("p", [0.0, 0.25])
 def test_combine(T, d_out, E, k, dtype, cf, p):
     cfg, t, dest, act = _combine_case(T, d_out, E, k, dtype, cf, T + k)
@@ -185,15 +187,16 @@ def test_combine(T, d_out, E, k, dtype, cf, p):
     assert (_f64(dg)[dest < 0] == 0).all()
 
 
+@pytest.mark.parametrize("k", [3, 8])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_without_dropout_it_is_the_combine(dtype):
-    cfg, t, dest, act = _combine_case(300, 136, 8, 3, dtype, 0.6, 5)
+def test_without_dropout_it_is_the_combine(dtype, k):
+    cfg, t, dest, act = _combine_case(300, 136, 8, k, dtype, 0.6, 5)
     a, b = (torch.empty((300, 136), dtype=act, device="cuda") for _ in range(2))
     api.moe_combine(cfg, t["y"], t["dest"], t["gates"], a)
     api.moe_combine_dropout(cfg, 0.0, 1, 2, 0, t["y"], t["dest"], t["gates"], None, b)
     assert torch.equal(a, b)
     da, db = (torch.zeros_like(t["y"]) for _ in range(2))
-    ga, gb = (torch.empty((300, 3), device="cuda") for _ in range(2))
+    ga, gb = (torch.empty((300, k), device="cuda") for _ in range(2))
     api.moe_combine_backward(cfg, t["dy"], t["y"], t["dest"], t["gates"], da, ga)
     api.moe_combine_dropout_backward(cfg, 0.0, 1, 2, 0, t["dy"], t["y"], t["dest"], t["gates"], db,
                                      gb)
@@ -214,19 +217,20 @@ def test_combine_drops_the_same_elements_as_dropout():
     assert torch.equal(fused == 0, both == 0)
 
 
-def test_combine_backward_ignores_dropped_infinities():
-    cfg, t, dest, act = _combine_case(40, 64, 8, 2, "bf16", 0.0, 7)
+@pytest.mark.parametrize("k", [2, 8])
+def test_combine_backward_ignores_dropped_infinities(k):
+    cfg, t, dest, act = _combine_case(40, 64, 8, k, "bf16", 0.0, 7)
     keep = torch.from_numpy(Q.keep_mask(40, 64, 0.5, 1, 1)).cuda()
     args = (cfg, 0.5, 1, 1, 0)
 
     def run(dy, y):
-        dyp, dg = torch.zeros_like(y), torch.empty((40, 2), device="cuda")
+        dyp, dg = torch.zeros_like(y), torch.empty((40, k), device="cuda")
         api.moe_combine_dropout_backward(*args, dy, y, t["dest"], t["gates"], dyp, dg)
         return dyp, dg
 
     dy = torch.where(keep, t["dy"], torch.full_like(t["dy"], float("nan")))
-    row = torch.zeros(80, dtype=torch.int64, device="cuda")
-    row[t["dest"].long().reshape(-1)] = torch.arange(40, device="cuda").repeat_interleave(2)
+    row = torch.zeros(40 * k, dtype=torch.int64, device="cuda")
+    row[t["dest"].long().reshape(-1)] = torch.arange(40, device="cuda").repeat_interleave(k)
     y = torch.where(keep[row], t["y"], torch.full_like(t["y"], float("inf")))
     for a, b in zip(run(t["dy"], t["y"]), run(dy, y)):
         assert torch.equal(a, b)
