@@ -109,17 +109,19 @@ def test_without_addends(T, base, dx_add):
     _check(i, _run(i, T, 136, 264, 3, 16, base, dx_add), base, dx_add)
 
 
-@pytest.mark.parametrize("T", [50, 1500, 4900, 6600])
+@pytest.mark.parametrize("T,n,d,w", [
+    (50, 6, 72, 136), (3, 8, 136, 328), (4, 18, 72, 136), (1500, 6, 72, 136), (4900, 6, 72, 136),
+    (6600, 6, 72, 136)])
 @pytest.mark.parametrize("ids", ["none", "one", "last"])
-def test_extreme_groups(T, ids):
+def test_extreme_groups(T, n, d, w, ids):
     """No token with an adapter; all on one; only the last token on the last."""
-    i = _inputs(T, 72, 136, 6, 16, seed=2)
+    i = _inputs(T, d, w, n, 16, seed=2)
     i["ids"][:] = {"none": -1, "one": 2, "last": -5}[ids]
     if ids == "last":
-        i["ids"][-1] = 5
-    got = _run(i, T, 72, 136, 6, 16)
+        i["ids"][-1] = n - 1
+    got = _run(i, T, d, w, n, 16)
     _check(i, got)
-    idle = [a for a in range(6) if not (i["ids"] == a).any()]
+    idle = [a for a in range(n) if not (i["ids"] == a).any()]
     assert (got[3][idle] == 0).all() and (got[4][idle] == 0).all()
 
 
