@@ -852,13 +852,16 @@ bool use_tc(int T, int n, int r) {
 size_t term_rows(int T, int n) { return (size_t)max_tiles(T, n) * tile_rows(T, n); }
 
 // Chunks of the gradient's rows: two CTAs an SM, but 256 rows at least (a part's
-// trip through memory costs more) and kGradMax at most.  With 128 at least, 1000
-// rows of 2048, rank 64, took 49 us forward and backward against 47; with 512, 64
-// rows on 64 adapters of 4096, rank 16, 59 against 53.
+// trip through memory costs more), unless adapters are so small that a chunk
+// would walk more than about four of them, and kGradMax at most.  Forward and
+// backward on B200, us: 1000 rows of 2048 on 4 adapters, rank 64, 47, with 128
+// rows at least 49; 64 rows of 4096 on 64, rank 16, 53, with 512 at least 59; 32
+// rows of 408 on 27, rank 40, 27, by rows alone 41.
 int grad_chunks(const moe_config_t& c, int n) {
   const int mb = ceil_div(c.d, kGradCols) + ceil_div(c.d_out, kGradCols);
   const int64_t rows = (int64_t)term_rows(c.T, n);
-  const int even = (int)std::min<int64_t>(2 * device_sm_count() / mb, rows / 256);
+  const int even = (int)std::min<int64_t>(2 * device_sm_count() / mb,
+                                          std::max<int64_t>(rows / 256, n / 4));
   return std::max(std::max(1, even), (int)((rows + kGradMax - kGradRows - 1) /
                                            (kGradMax - kGradRows)));
 }
@@ -981,12 +984,12 @@ cudaError_t launch_adapter_grad(const moe_config_t& c, int n, int r, void* plan,
   const int N = ceil_div(3 * r, 16) * 16, boxes = ceil_div(N, 64);
   int cols = 32;
   while (cols < N) cols *= 2;
-  // One chunk of rows has no parts to add; with few adapters it spares the
-  // launch that would write the rowless ones' zeros.  All of a step, us (without
+  // One chunk of rows has no parts to add, and few adapters: their zeros, where
+  // they have no rows, are written without a launch.  All of a step, us (without
   // that launch against with): 333 rows, 5 adapters 27.4 / 30.3; 300 rows, 4
-  // adapters of 4096 41.3 / 44.0; but 4 rows, 18 adapters 34.7 / 30.5.
+  // adapters of 4096 41.3 / 44.0.
   const int chunks = grad_chunks(c, n);
-  const int fold = chunks == 1 && n <= 8;
+  const int fold = chunks == 1;
   const GradArgs g{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(dy),
                    dA, dB,
                    reinterpret_cast<float*>(w + W.part),
