@@ -144,9 +144,8 @@ __device__ __forceinline__ void store_values(float* row, int E, int gl, const fl
 // so are inv and lse.
 // exp(d), d = l - m <= 0, is 2^(d log2 e): one product and the hardware's 2^x,
 // within 2.3 |d| + 4 half steps of fp32.  (One fused 2^(l log2e - m log2e) would
-// overflow for logits at the type's lowest value.)  With expf, whose exact range
-// reduction is six more instructions a logit, the forward's first launch took 57
-// us, against 44, at 131072 x 256.
+// overflow for logits at the type's lowest value.)  With expf the forward's first
+// launch took 57 us, against 44, at 131072 x 256.
 template <typename L>
 __device__ __forceinline__ void softmax_terms(float (&v)[L::NV], bool act, float& inv,
                                               float& lse) {
