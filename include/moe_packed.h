@@ -43,8 +43,9 @@ extern "C" {
  *   losses       (2) fp32 out (0 where nothing is counted)
  *   ws           moe_balance_workspace_size bytes, its own workspace; first
  *                256 bytes as in moe_workspace_init / moe_device_status
- * fp32 sums per 8 to 64 tokens, fp64 above; fixed orders, no floating-point
- * atomics.  T * top_k and n_seqs at most 2^30. */
+ * Sums over tokens: fp32 for at most 64 tokens (and 8 such sums in pairs up to
+ * T = 303103), fp64 above; fixed orders, no floating-point atomics.  T * top_k
+ * and n_seqs at most 2^30. */
 size_t moe_balance_workspace_size(const moe_config_t* cfg, int32_t n_seqs);
 int moe_balance_loss(const moe_config_t* cfg, int32_t n_seqs, const int32_t* seq_offsets,
                      const uint8_t* token_mask, const float* logits,

@@ -26,9 +26,11 @@
 // meet them; each such piece gets the slot (warp + s) of the partial sums,
 // which no other piece has (going to the next warp or the next sequence
 // raises it by at least one), so no scan over the sequences is needed.  Where
-// one sequence covers all 8 warps of a CTA, their sums are added in warp
-// order and only the first warp's slot is written.  The second launch adds a
-// sequence's slots in a fixed order in fp64.
+// one sequence covers all 8 warps of a CTA, their sums are added and only the
+// first warp's slot is written.  The second launch adds a sequence's slots in a
+// fixed order in fp64.  A warp's fp32 sums cover at most 64 tokens, and a CTA's 8 of
+// them are added in pairs; in batches whose warps own more (C > 64, above 303103
+// tokens) both go on in fp64, blocks of 64 tokens in shared memory.
 #include "moe_device.cuh"
 #include "moe_internal.h"
 
@@ -36,6 +38,7 @@ namespace moe {
 namespace {
 
 constexpr int kLogWarps = 3, kWarps = 1 << kLogWarps;
+constexpr int kLogSum = 6, kSumTokens = 1 << kLogSum;   // tokens of a warp's fp32 sums
 
 // The number of i in [1, S] with off[i] <= t, for non-decreasing off: the
 // sequence that holds token t if off[0] <= t < off[S].  32 samples a round.
@@ -136,6 +139,17 @@ __device__ __forceinline__ void store_values(float* row, int E, int gl, const fl
       const int e = L::expert(gl, i);
       if (e < E) row[e] = v[i];
     }
+  }
+}
+
+// This lane's values into a row of fp64 sums (first), or added to it.
+template <typename L>
+__device__ __forceinline__ void add_values(double* row, int E, int gl, bool first,
+                                           const float (&v)[L::NV]) {
+#pragma unroll
+  for (int i = 0; i < L::NV; ++i) {
+    const int e = L::expert(gl, i);
+    if (e < E) row[e] = (first ? 0.0 : row[e]) + (double)v[i];
   }
 }
 
@@ -358,10 +372,46 @@ __device__ __forceinline__ bool last_cta(unsigned* done) {
   return last;
 }
 
-// FUSED: the last CTA also adds up the sequences (few CTAs and sequences:
+// kFused: the last CTA also adds up the sequences (few CTAs and sequences:
 // the second launch would cost more than its work; 64 x 8 in both directions: 11.6
 // us against 14.0).
-template <typename L, bool FUSED>
+// kLong: a warp owns more than kSumTokens tokens, and keeps fp64 sums of its blocks of
+// that many in dynamic shared memory (fp64 for shorter batches too cost 16384 x 64
+// in both directions 21.5 us against 20.5).
+enum PartialForm { kFused, kPlain, kLong };
+constexpr int kWideBytes = (kWarps * 256 + kWarps) * 8;   // kLong's p, then z
+
+// a[0] + ... + a[kWarps - 1], `step` apart, in pairs.
+__device__ __forceinline__ float pair_sum(const float* a, int step) {
+  float v[kWarps];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v[w] = a[w * step];
+#pragma unroll
+  for (int o = 1; o < kWarps; o *= 2)
+#pragma unroll
+    for (int w = 0; w < kWarps; w += 2 * o) v[w] += v[w + o];
+  return v[0];
+}
+
+__device__ __forceinline__ float wide_sum(const double* a, int step) {
+  double v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v += a[w * step];
+  return (float)v;
+}
+
+// This lane's values and z, summed over the warp's groups of G lanes.
+template <int G, int NV>
+__device__ __forceinline__ void warp_groups_sum(float (&v)[NV], float& z) {
+#pragma unroll
+  for (int o = 16; o >= G; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+}
+
+template <typename L, PartialForm FORM>
 __global__ void __launch_bounds__(256, 4)
     balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                            const int32_t* __restrict__ off, const uint8_t* __restrict__ mask,
@@ -373,6 +423,7 @@ __global__ void __launch_bounds__(256, 4)
   __shared__ int32_t red_n[kWarps];
   __shared__ float red_z[kWarps];
   __shared__ int first_seq[kWarps];
+  extern __shared__ double wide[];   // kLong
   constexpr int G = L::G, W = L::W, NV = L::NV;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane / G, gl = lane % G;
@@ -389,6 +440,8 @@ __global__ void __launch_bounds__(256, 4)
   if (lane == 0) first_seq[warp] = s;
   __syncthreads();
   const int s0 = first_seq[0];
+  double* wide_p = wide + warp * 256;
+  double* wide_z = wide + kWarps * 256 + warp;
   auto counted = [&](int t, int end) {
     return t < end && (mask == nullptr || __ldg(mask + t) != 0);
   };
@@ -429,6 +482,10 @@ __global__ void __launch_bounds__(256, 4)
         else report_error(err, kDevBadExpertIndex);
       }
     }
+    if (FORM == kLong && b >= e1) {   // a warp of a merged CTA without tokens
+      for (int e = lane; e < E; e += 32) wide_p[e] = 0.0;
+      if (lane == 0) *wide_z = 0.0;
+    }
     float acc[NV], z = 0.f;
     int n = 0;
 #pragma unroll
@@ -448,18 +505,30 @@ __global__ void __launch_bounds__(256, 4)
         z = fmaf(lse, lse, z);
         ++n;
       }
-    }
+      if constexpr (FORM == kLong) {
+        const int sofar = tb + W - b;
+        if (sofar % kSumTokens != 0 && tb + W < e1) continue;
+        warp_groups_sum<G, NV>(acc, z);
+        const bool first = sofar <= kSumTokens;
+        if (g == 0) add_values<L>(wide_p, E, gl, first, acc);
+        if (lane == 0) *wide_z = (first ? 0.0 : *wide_z) + (double)z;
 #pragma unroll
-    for (int o = 16; o >= G; o >>= 1) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      z += __shfl_xor_sync(0xffffffffu, z, o);
-      n += __shfl_xor_sync(0xffffffffu, n, o);
+        for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+        z = 0.f;
+      }
     }
+    if constexpr (FORM != kLong) warp_groups_sum<G, NV>(acc, z);
+#pragma unroll
+    for (int o = 16; o >= G; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     __syncwarp();
     if (!merged) {
       const size_t slot = (size_t)gw + s;
-      if (g == 0) store_values<L>(part.p + slot * E, E, gl, acc);
+      if constexpr (FORM == kLong) {
+        for (int e = lane; e < E; e += 32) part.p[slot * E + e] = (float)wide_p[e];
+        z = (float)*wide_z;
+      } else {
+        if (g == 0) store_values<L>(part.p + slot * E, E, gl, acc);
+      }
       for (int e = lane; e < E; e += 32) part.c[slot * E + e] = hist[warp][e];
       if (lane == 0) {
         part.n[slot] = n;
@@ -468,7 +537,7 @@ __global__ void __launch_bounds__(256, 4)
       __syncwarp();
       continue;
     }
-    if (g == 0) store_values<L>(red[warp], E, gl, acc);
+    if (FORM != kLong && g == 0) store_values<L>(red[warp], E, gl, acc);
     if (lane == 0) {
       red_n[warp] = n;
       red_z[warp] = z;
@@ -476,30 +545,23 @@ __global__ void __launch_bounds__(256, 4)
     __syncthreads();
     const size_t slot = (size_t)blockIdx.x * kWarps + s;
     for (int e = threadIdx.x; e < E; e += 256) {
-      float v = 0.f;
       int c = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        v += red[w][e];
-        c += hist[w][e];
-      }
-      part.p[slot * E + e] = v;
+      for (int w = 0; w < kWarps; ++w) c += hist[w][e];
+      part.p[slot * E + e] =
+          FORM == kLong ? wide_sum(wide + e, 256) : pair_sum(&red[0][e], 256);
       part.c[slot * E + e] = c;
     }
     if (threadIdx.x == 0) {
-      float v = 0.f;
       int c = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        v += red_z[w];
-        c += red_n[w];
-      }
-      part.z[slot] = v;
+      for (int w = 0; w < kWarps; ++w) c += red_n[w];
+      part.z[slot] = FORM == kLong ? wide_sum(wide + kWarps * 256, 1) : pair_sum(red_z, 1);
       part.n[slot] = c;
     }
     break;
   }
-  if constexpr (FUSED) {
+  if constexpr (FORM == kFused) {
     __shared__ FinishSmem<256> sm;
     if (!last_cta(done)) return;
     for (int s = 0; s < S; ++s) finish_sequence(sm, part, off, s, T, E, k, lc, EP, out, err);
@@ -676,10 +738,12 @@ cudaError_t launch_balance_loss(const moe_config_t& c, int S, const int32_t* off
   if (grid > 0) {
     const cudaError_t e = by_width(c.E, vector_rows(c.E, logits, nullptr), [&](auto lanes) {
       using W = decltype(lanes);
-      const auto kern =
-          fused ? balance_partial_kernel<W, true> : balance_partial_kernel<W, false>;
-      return launch_kernel(kern, grid, 256, 0, s, 0, logits, idx, off, mask, c.T, c.E, c.top_k, S,
-                           lc, part, EP, out, done, err);
+      const bool wide = lc > kLogSum;
+      const auto kern = fused  ? balance_partial_kernel<W, kFused>
+                        : wide ? balance_partial_kernel<W, kLong>
+                               : balance_partial_kernel<W, kPlain>;
+      return launch_kernel(kern, grid, 256, wide ? kWideBytes : 0, s, 0, logits, idx, off, mask,
+                           c.T, c.E, c.top_k, S, lc, part, EP, out, done, err);
     });
     if (e != cudaSuccess || fused) return e;
   }
