@@ -147,7 +147,7 @@ int moe_combine_dropout_backward(const moe_config_t* cfg, const moe_dropout_t* d
  *   bf16; scale (n_adapters) fp32; base (T, d_out) bf16 or NULL (0);
  *   output (T, d_out) bf16 out, may be base, must not overlap x;
  *   u (T, rank) fp32 out or NULL: kept for the backward (rows of tokens
- *   without an adapter are left untouched)
+ *   without an adapter are left untouched); output is the same either way
  * moe_adapter_backward, for dy = dLoss/d output (T, d_out) bf16:
  *   v[t] = scale_a dy[t] B_a^T
  *   dx[t] = dx_add[t] + v[t] A_a^T        (dx_add alone without an adapter)

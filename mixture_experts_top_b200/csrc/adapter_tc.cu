@@ -41,9 +41,10 @@ constexpr int kProducers = 128;     // threads of the row producers
 constexpr int kMmaWarp = 18, kWeightWarp = 19;
 // Input stages a block of D1's sum: the truncation of 256 columns' sums leaves u
 // and v within 2e-7 of exact, 512's within 4e-7, which u's and v's products, the
-// gradients, would show; blocks of 1024 are 1-2 % faster and serve a forward
-// pass that keeps no u, whose output is bf16.
-constexpr int kFlushKept = 2, kFlush = 8;
+// gradients, would show.  (A forward pass that keeps no u could take blocks of 1024:
+// 8192 x 4096, rank 16, 47.3 us against 47.4, but its output would have other bits
+// than one that keeps it.)
+constexpr int kFlush = 2;
 constexpr int kAux = 1024;          // barriers, tmem address, rows
 constexpr int kMaxStages = 8;
 
@@ -74,11 +75,10 @@ struct TcShape {
   int smem;
   int u_col, d2_col;   // tensor-memory columns
   int groups;      // epilogue groups that take output stages, a D2 buffer each
-  int flush;       // input stages a block of D1's sum
 };
 
 template <bool BWD>
-TcShape tc_shape(int r, bool kept) {
+TcShape tc_shape(int r) {
   TcShape t;
   t.rp = ceil_div(r, 16) * 16;
   t.nb = ceil_div(t.rp, 64);
@@ -95,7 +95,6 @@ TcShape tc_shape(int r, bool kept) {
   t.u_col = t.nb * 64;
   t.d2_col = t.u_col + (BWD ? 3 : 2) * t.rp / 2;
   t.groups = std::min(kGroups, (512 - t.d2_col) / (BWD ? 64 : 128));
-  t.flush = kept ? kFlushKept : kFlush;
   return t;
 }
 
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
   const int nk = ceil_div_dev(K, kKc), nn = ceil_div_dev(N, NC);
-  const int nf = ceil_div_dev(nk, sh.flush);
+  const int nf = ceil_div_dev(nk, kFlush);
 
   if (warp == kWeightWarp) {
     // ------------------------------------------------------ weight producer
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
                    (in_block | kk) != 0 ? 1u : 0u);
       if (lane == 0) mbar_arrive_n(&empty[slot], 3);
       umma_commit_elect(&empty[slot]);
-      if (++in_block == sh.flush || s == nk - 1) {
+      if (++in_block == kFlush || s == nk - 1) {
         umma_commit_elect(&d1_full[block & 1]);
         ++block;
         in_block = 0;
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) low_rank_tc_kernel(
 
 template <bool BWD>
 cudaError_t run(const LowRankArgs& g, int tiles, cudaStream_t s) {
-  const TcShape sh = tc_shape<BWD>(g.r, BWD || g.u != nullptr);
+  const TcShape sh = tc_shape<BWD>(g.r);
   const auto kern = low_rank_tc_kernel<BWD>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), 227 * 1024);
   if (e != cudaSuccess) return e;
