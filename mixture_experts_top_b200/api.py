@@ -391,7 +391,10 @@ def moe_forward(cfg, x, W_router, logit_bias, noise, W_in, W_up, W_out, output, 
 
 def _arg(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     """Pointer of a contiguous tensor of this type and shape (None: any) on
-    CUDA device `dev`, the current one."""
+    CUDA device `dev`, the current one.  No tensor is NULL, which the library
+    takes for an optional argument and refuses by name for another."""
+    if t is None:
+        return None
     if (t.dtype is dtype and (shape is None or t.shape == shape) and t.get_device() == dev
             and t.is_contiguous()):
         return t.data_ptr()
@@ -404,8 +407,23 @@ def _arg(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name: str, dtype, shape, dev: int) -> Optional[int]:
-    return None if t is None else _arg(t, name, dtype, shape, dev)
+def _buf(t, name: str, u8, dev: int):
+    """Pointer and bytes of a workspace or plan."""
+    return _arg(t, name, u8, None, dev), 0 if t is None else t.numel()
+
+
+def _mask(t, T: int, dev: int) -> Optional[int]:
+    """A token mask: uint8, or bool (bytes of 0 and 1)."""
+    if t is None:
+        return None
+    import torch
+    return _arg(t, "token_mask", torch.bool if t.dtype is torch.bool else torch.uint8, (T,), dev)
+
+
+def _not_null(t, name: str, where: str) -> None:
+    """The library's refusal, for a tensor whose type or shape is read before the call."""
+    if t is None:
+        raise MoeError(MOE_ERR_INVALID_ARG, where, f"{name} is NULL")
 
 
 def _where(stream):
@@ -460,15 +478,15 @@ def alloc_balance_workspace(cfg: MoeConfig, n_seqs: int, device="cuda", stream=N
 def moe_balance_loss(cfg, seq_offsets, token_mask, logits, expert_indices, counts, prob_mean,
                      tokens, losses, ws, stream=None) -> None:
     """seq_offsets (n_seqs+1) int32 or None (one sequence: all tokens);
-    token_mask (T) uint8 or None; see include/moe_packed.h for the outputs."""
+    token_mask (T) uint8 or bool, or None; see include/moe_packed.h for the outputs."""
     import torch
     f32, i32 = torch.float32, torch.int32
     dev, st = _where(stream)
     n, off = _seqs(seq_offsets, i32, dev)
     T, E = cfg.T, cfg.E
-    wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
+    wp, wn = _buf(ws, "ws", torch.uint8, dev)
     _check(load_library().moe_balance_loss(
-        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,), dev),
+        ctypes.byref(cfg), n, off, _mask(token_mask, T, dev),
         _arg(logits, "logits", f32, (T, E), dev),
         _arg(expert_indices, "expert_indices", i32, (T, cfg.top_k), dev),
         _arg(counts, "counts", i32, (n, E), dev), _arg(prob_mean, "prob_mean", f32, (n, E), dev),
@@ -483,9 +501,9 @@ def moe_balance_loss_backward(cfg, seq_offsets, token_mask, logits, counts, toke
     dev, st = _where(stream)
     n, off = _seqs(seq_offsets, i32, dev)
     T, E = cfg.T, cfg.E
-    wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
+    wp, wn = _buf(ws, "ws", torch.uint8, dev)
     _check(load_library().moe_balance_loss_backward(
-        ctypes.byref(cfg), n, off, _opt(token_mask, "token_mask", torch.uint8, (T,), dev),
+        ctypes.byref(cfg), n, off, _mask(token_mask, T, dev),
         _arg(logits, "logits", f32, (T, E), dev), _arg(counts, "counts", i32, (n, E), dev),
         _arg(tokens, "tokens", i32, (n + 2,), dev), _arg(dlosses, "dlosses", f32, (2,), dev),
         _arg(dlogits, "dlogits", f32, (T, E), dev), wp, wn, st),
@@ -502,7 +520,7 @@ def moe_route_backward_add(cfg, x, W_router, logits, expert_indices, gates, f, d
     _check(load_library().moe_route_backward_add(
         ctypes.byref(cfg), _ptr(x), _ptr(W_router), _ptr(logits), _ptr(expert_indices),
         _ptr(gates), _ptr(f), _ptr(dgates), _ptr(daux), int(T_batch), add, _ptr(dx),
-        _ptr(dW_router), _ptr(dbias), _ptr(dlogits), _ptr(ws), ws.numel(), st),
+        _ptr(dW_router), _ptr(dbias), _ptr(dlogits), _ptr(ws), 0 if ws is None else ws.numel(), st),
         "moe_route_backward_add")
 
 
@@ -519,6 +537,7 @@ def moe_dropout(cfg, p, seed, offset, token_base, x, add, out, stream=None) -> N
     """out = add + dropout(x) over (T, width) rows, bf16 or fp32; add may be
     None, out may be x or add."""
     import torch
+    _not_null(x, "x", "moe_dropout")
     dt, shape = x.dtype, x.shape
     if dt is not torch.bfloat16 and dt is not torch.float32:
         raise ValueError(f"x must be bfloat16 or float32, got {dt}")
@@ -529,7 +548,7 @@ def moe_dropout(cfg, p, seed, offset, token_base, x, add, out, stream=None) -> N
     _check(load_library().moe_dropout(
         ctypes.byref(cfg), ctypes.byref(d), shape[1],
         DTYPES["bf16"] if dt is torch.bfloat16 else DTYPES["f32"], _arg(x, "x", dt, None, dev),
-        _opt(add, "add", dt, shape, dev), _arg(out, "out", dt, shape, dev), st),
+        _arg(add, "add", dt, shape, dev), _arg(out, "out", dt, shape, dev), st),
         "moe_dropout")
 
 
@@ -543,7 +562,7 @@ def moe_combine_dropout(cfg, p, seed, offset, token_base, y_perm, dest, gates, r
     _check(load_library().moe_combine_dropout(
         ctypes.byref(cfg), ctypes.byref(d), _arg(y_perm, "y_perm", f32, (T * k, w), dev),
         _arg(dest, "dest", torch.int32, (T, k), dev), _arg(gates, "gates", f32, (T, k), dev),
-        _opt(residual, "residual", act, (T, w), dev), _arg(output, "output", act, (T, w), dev),
+        _arg(residual, "residual", act, (T, w), dev), _arg(output, "output", act, (T, w), dev),
         st), "moe_combine_dropout")
 
 
@@ -587,14 +606,15 @@ def moe_adapter_plan(cfg, n_adapters, token_adapter, plan, stream=None) -> None:
     """Groups the tokens by adapter: token_adapter (T) int32, negative for none."""
     import torch
     dev, st = _where(stream)
-    pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
+    pp, pn = _buf(plan, "plan", torch.uint8, dev)
     _check(load_library().moe_adapter_plan(
         ctypes.byref(cfg), int(n_adapters),
         _arg(token_adapter, "token_adapter", torch.int32, (cfg.T,), dev), pp, pn, st),
         "moe_adapter_plan")
 
 
-def _adapter_shape(cfg, A):
+def _adapter_shape(cfg, A, where):
+    _not_null(A, "A", where)
     if A.dim() != 3 or A.shape[1] != cfg.d:
         raise ValueError(f"A must have shape (n_adapters, {cfg.d}, rank), got {tuple(A.shape)}")
     return A.shape[0], A.shape[2]
@@ -604,30 +624,30 @@ def moe_adapter(cfg, plan, x, A, B, scale, base, output, u, stream=None) -> None
     """output = base + scale x A B by each token's adapter; base and u may be None."""
     import torch
     bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
-    n, r = _adapter_shape(cfg, A)
+    n, r = _adapter_shape(cfg, A, "moe_adapter")
     dev, st = _where(stream)
-    pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
+    pp, pn = _buf(plan, "plan", torch.uint8, dev)
     _check(load_library().moe_adapter(
         ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d), dev),
         _arg(A, "A", bf, None, dev),
         _arg(B, "B", bf, (n, r, w), dev), _arg(scale, "scale", f32, (n,), dev),
-        _opt(base, "base", bf, (T, w), dev), _arg(output, "output", bf, (T, w), dev),
-        _opt(u, "u", f32, (T, r), dev), st), "moe_adapter")
+        _arg(base, "base", bf, (T, w), dev), _arg(output, "output", bf, (T, w), dev),
+        _arg(u, "u", f32, (T, r), dev), st), "moe_adapter")
 
 
 def moe_adapter_backward(cfg, plan, x, u, dy, A, B, scale, dx_add, dx, dA, dB, ws,
                          stream=None) -> None:
     import torch
     bf, f32, T, w = torch.bfloat16, torch.float32, cfg.T, cfg.d_out
-    n, r = _adapter_shape(cfg, A)
+    n, r = _adapter_shape(cfg, A, "moe_adapter_backward")
     dev, st = _where(stream)
-    pp, pn = _arg(plan, "plan", torch.uint8, None, dev), plan.numel()
-    wp, wn = _arg(ws, "ws", torch.uint8, None, dev), ws.numel()
+    pp, pn = _buf(plan, "plan", torch.uint8, dev)
+    wp, wn = _buf(ws, "ws", torch.uint8, dev)
     _check(load_library().moe_adapter_backward(
         ctypes.byref(cfg), n, r, pp, pn, _arg(x, "x", bf, (T, cfg.d), dev),
         _arg(u, "u", f32, (T, r), dev),
         _arg(dy, "dy", bf, (T, w), dev), _arg(A, "A", bf, None, dev),
         _arg(B, "B", bf, (n, r, w), dev),
-        _arg(scale, "scale", f32, (n,), dev), _opt(dx_add, "dx_add", f32, (T, cfg.d), dev),
+        _arg(scale, "scale", f32, (n,), dev), _arg(dx_add, "dx_add", f32, (T, cfg.d), dev),
         _arg(dx, "dx", f32, (T, cfg.d), dev), _arg(dA, "dA", f32, A.shape, dev),
         _arg(dB, "dB", f32, (n, r, w), dev), wp, wn, st), "moe_adapter_backward")
