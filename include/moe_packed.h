@@ -26,6 +26,12 @@ extern "C" {
  *   losses[0]   = 1/S+ sum_s E sum_e f[s,e] P[s,e]
  *   losses[1]   = 1/N sum_t (log sum_e exp logits[t,e])^2
  * One sequence that holds the whole batch gives moe_dispatch's aux_loss.
+ * A batch split over ranks: each rank takes whole sequences (one that is cut
+ * would need its f and P over all its tokens, which no call forms).  With N_r
+ * and S+_r a rank's, N and S+ their sums over the ranks, the whole batch's
+ * losses are the sums of S+_r / S+ losses_r[0] and N_r / N losses_r[1], and a
+ * rank's dlogits are the whole batch's for dlosses (S+_r / S+ dlosses[0],
+ * N_r / N dlosses[1]).
  *   n_seqs       sequences, >= 1
  *   seq_offsets  (n_seqs+1) int32, 0 <= non-decreasing <= T, or NULL with
  *                n_seqs = 1: all T tokens.  Tokens before the first or at and
