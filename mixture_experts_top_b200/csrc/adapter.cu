@@ -485,9 +485,12 @@ __global__ void __launch_bounds__(256) low_rank_kernel(LowRankArgs g) {
 // boxes of 64 columns x 32 rows).
 // The rows, by tile slot, are cut into equal chunks, as many as give every SM
 // two CTAs, whatever the adapters' sizes; a CTA walks the adapters that meet its
-// chunk.  One that lies in it whole goes straight to the gradient; the part of
-// another in chunk p goes to the slot p + a, which no other part has, and the
-// last launch adds an adapter's parts in order.  (One CTA per adapter and part
+// chunk.  One that lies in it whole goes straight to the gradient; the part in
+// chunk p of another, a, that starts in chunk p0 goes to the slot
+// p + min(a, p0), and the last launch adds an adapter's parts in order.  (Of the
+// cut adapters each starts in a chunk of its own and ends no later than the next one
+// starts, so that both a and p0 grow from one to the next: no two parts share a
+// slot, and there are fewer than chunks + min(n, chunks) of them.)  (One CTA per adapter and part
 // instead ran in two uneven waves: 33 us against 25 at 8192 x 2048, rank 64.)
 // Warps 0-3 read tensor memory, 4-7 gather x's rows into the stages by
 // cp.async, 8 issues the MMAs, 9 loads the terms by TMA (its issue would hold
@@ -519,7 +522,7 @@ struct GradArgs {
   const __nv_bfloat16* dy;  // (T, d_out)
   float* dA;                // (n, d, r)
   float* dB;                // (n, r, d_out)
-  float* part;              // (slots, r (d + d_out)): parts of split adapters, dA's then dB's
+  float* part;              // (part_slots, r (d + d_out)): parts of cut adapters, dA's then dB's
   const int32_t* header;
   const int32_t* offsets;
   const int32_t* rows;
@@ -543,11 +546,13 @@ __device__ __forceinline__ int chunk_rows(const GradArgs& g) {
 // tile slot is at `at`.
 struct ChunkParts {
   const GradArgs& g;
-  int lo, hi, a, at, i0, i1;
+  int lo, hi, len, a, at, i0, i1;
   bool whole;   // all of the adapter's rows
-  // a0: the last adapter that starts at or before the chunk
-  __device__ ChunkParts(const GradArgs& g_, int lo_, int hi_, int a0)
-      : g(g_), lo(lo_), hi(hi_), a(a0 - 1) {}
+  // a0: the last adapter that starts at or before the chunk; len: rows of a chunk
+  __device__ ChunkParts(const GradArgs& g_, int lo_, int hi_, int len_, int a0)
+      : g(g_), lo(lo_), hi(hi_), len(len_), a(a0 - 1) {}
+  // The part's slot.
+  __device__ size_t slot(int chunk) const { return (size_t)(chunk + min(a, at / len)); }
   __device__ bool next() {
     while (++a < g.n) {
       const int o = __ldg(g.offsets + a), cnt = __ldg(g.offsets + a + 1) - o;
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(kGradThreads, 2)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
-  ChunkParts part(g, lo, hi, a0);
+  ChunkParts part(g, lo, hi, len, a0);
 
   if (warp >= 4 && warp < 8) {
     // ---- producers
@@ -687,7 +692,7 @@ __global__ void __launch_bounds__(kGradThreads, 2)
       const int a = part.a;
       float* out = part.whole
                        ? (isA ? g.dA + (size_t)a * dsz : g.dB + (size_t)a * bsz)
-                       : g.part + (size_t)(chunk + a) * (dsz + bsz) + (isA ? 0 : dsz);
+                       : g.part + part.slot(chunk) * (dsz + bsz) + (isA ? 0 : dsz);
       for (int j0 = 0; j0 < r; j0 += 16) {
         uint32_t t[2][3][8];
 #pragma unroll
@@ -807,7 +812,7 @@ __global__ void __launch_bounds__(256) adapter_reduce_kernel(GradArgs g) {
   const int parts = cnt > 0 ? (at + cnt - 1) / len - p0 + 1 : 0;
   if (parts == 1) return;
   const size_t dsz = (size_t)g.d * g.r, bsz = (size_t)g.d_out * g.r, all = dsz + bsz;
-  const float* src = g.part + (size_t)(p0 + a) * all;
+  const float* src = g.part + (size_t)(p0 + min(a, p0)) * all;
   for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all;
        i += (size_t)gridDim.x * 1024) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -866,6 +871,9 @@ int grad_chunks(const moe_config_t& c, int n) {
                                            (kGradMax - kGradRows)));
 }
 
+// Slots of the parts (adapter_grad_kernel).
+size_t part_slots(int chunks, int n) { return (size_t)chunks + std::min(n, chunks); }
+
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
@@ -886,7 +894,7 @@ AdapterWsLayout adapter_ws_layout(const moe_config_t& c, int n, int r) {
   L.v = 0;
   L.u = up256(term_rows(c.T, n) * r * 6);
   L.part = 2 * L.u;
-  L.total = L.part + up256((size_t)(grad_chunks(c, n) + n) * r * ((size_t)c.d + c.d_out) * 4);
+  L.total = L.part + up256(part_slots(grad_chunks(c, n), n) * r * ((size_t)c.d + c.d_out) * 4);
   return L;
 }
 
