@@ -22,36 +22,25 @@
 namespace moe {
 namespace {
 
-// Block b of 8 elements: thread-strided, U blocks a thread with all their
-// loads issued first.  At 8192 x 4096 fp32 with an addend 403 MB in 59 us, the
-// measured copy rate and a little more.
-template <typename T, int U, bool ADD>
+// A block of 8 elements a thread.  At 8192 x 4096 fp32 with an addend 403 MB in 59
+// us, the measured copy rate and a little more.
+template <typename T, bool ADD>
 __global__ void __launch_bounds__(256)
     dropout_kernel(const T* x, const T* add, T* out, long long nblk, DropArgs d) {
   pdl_wait_and_release();
   const uint64_t offset = drop_offset(d);
-  const long long b0 = (long long)blockIdx.x * (256 * U) + threadIdx.x;
-  float v[U][8], a[U][8];
+  const long long b = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (b >= nblk) return;
+  float v[8], a[8];
+  load_row8(x + b * 8, v);
+  if (ADD) load_row8(add + b * 8, a);
+  const uint32_t keep = drop_keep8(d, offset, d.block0 + (uint64_t)b);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long b = b0 + 256 * u;
-    if (b < nblk) {
-      load_row8(x + b * 8, v[u]);
-      if (ADD) load_row8(add + b * 8, a[u]);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float w = (keep >> i) & 1u ? v[i] * d.scale : 0.f;
+    v[i] = ADD ? a[i] + w : w;
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long b = b0 + 256 * u;
-    if (b >= nblk) break;
-    const uint32_t keep = drop_keep8(d, offset, d.block0 + (uint64_t)b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float w = (keep >> i) & 1u ? v[u][i] * d.scale : 0.f;
-      v[u][i] = ADD ? a[u][i] + w : w;
-    }
-    store_row8(out + b * 8, v[u]);
-  }
+  store_row8(out + b * 8, v);
 }
 
 // The combine's two directions.  W warps of a CTA share a token (8 / W tokens
@@ -63,12 +52,11 @@ __global__ void __launch_bounds__(256)
 // top-2 the forward moves its 402 MB in 68 us and the backward its 604 MB in 94
 // (0.90 and 0.98 of the measured copy rate).  Above 4 slots, see the rings below.
 
-// The kept slots of token t in order (nk of them, the same in every lane):
-// their grouped rows and gates; lane i < nk holds its slot's number in `slot`.
-template <int K>
-__device__ __forceinline__ int load_slots(const int32_t* __restrict__ dest,
-                                          const float* __restrict__ gates, int t, int k,
-                                          int (&dj)[K], float (&gj)[K], int& slot) {
+// The kept slots of token t in order, nk of them, one a lane: lane i < nk holds the
+// i-th one's grouped row, gate and slot number.
+__device__ __forceinline__ int lane_slots(const int32_t* __restrict__ dest,
+                                          const float* __restrict__ gates, int t, int k, int& row,
+                                          float& gate, int& slot) {
   const int lane = threadIdx.x & 31;
   int d = -1;
   float g = 0.f;
@@ -78,13 +66,25 @@ __device__ __forceinline__ int load_slots(const int32_t* __restrict__ dest,
   }
   const unsigned kept = __ballot_sync(0xffffffffu, d >= 0);
   slot = (int)__fns(kept, 0, lane + 1) & 31;
+  row = __shfl_sync(0xffffffffu, d, slot);
+  gate = __shfl_sync(0xffffffffu, g, slot);
+  return __popc(kept);
+}
+
+// The same with every slot's grouped row and gate in every lane.
+template <int K>
+__device__ __forceinline__ int load_slots(const int32_t* __restrict__ dest,
+                                          const float* __restrict__ gates, int t, int k,
+                                          int (&dj)[K], float (&gj)[K], int& slot) {
+  int row;
+  float gate;
+  const int nk = lane_slots(dest, gates, t, k, row, gate, slot);
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    const int src = __shfl_sync(0xffffffffu, slot, j);
-    dj[j] = __shfl_sync(0xffffffffu, d, src);
-    gj[j] = __shfl_sync(0xffffffffu, g, src);
+    dj[j] = __shfl_sync(0xffffffffu, row, j);
+    gj[j] = __shfl_sync(0xffffffffu, gate, j);
   }
-  return __popc(kept);
+  return nk;
 }
 
 template <typename T, int K>
@@ -132,8 +132,33 @@ __global__ void __launch_bounds__(256, 4)
   }
 }
 
-// dgates: per lane in column order, a fixed butterfly over the warp, the
-// token's W warps in order.
+// A token's dgates from its lanes' partial sums: a fixed butterfly over the warp, the
+// token's W warps in order; 0 for dropped slots.  By the whole CTA.
+template <int K>
+__device__ __forceinline__ void store_dgates(float (&part)[K], float (&red)[8][K],
+                                             float* __restrict__ dgates, bool in, int t, int k,
+                                             int W, int nk, int slot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
+    if (lane == 0) red[warp][j] = part[j];
+  }
+  if (W > 1) __syncthreads();
+  else __syncwarp();
+  if (in && warp % W == 0) {
+    if (lane < nk) {
+      float v = red[warp][lane];
+      for (int w = 1; w < W; ++w) v += red[warp + w][lane];
+      dgates[(size_t)t * k + slot] = v;
+    }
+    // dropped slots
+    const unsigned kept = __reduce_or_sync(0xffffffffu, lane < nk ? 1u << slot : 0u);
+    if (lane < k && !(kept >> lane & 1u)) dgates[(size_t)t * k + lane] = 0.f;
+  }
+}
+
 template <typename T, int K>
 __global__ void __launch_bounds__(256, K <= 2 ? 4 : 3)
     combine_dropout_backward_kernel(const T* __restrict__ dy, const float* __restrict__ y_perm,
@@ -185,24 +210,7 @@ __global__ void __launch_bounds__(256, K <= 2 ? 4 : 3)
         }
     }
   }
-#pragma unroll
-  for (int j = 0; j < K; ++j) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
-    if (lane == 0) red[warp][j] = part[j];
-  }
-  if (W > 1) __syncthreads();
-  else __syncwarp();
-  if (in && warp % W == 0) {
-    if (lane < nk) {
-      float v = red[warp][lane];
-      for (int w = 1; w < W; ++w) v += red[warp + w][lane];
-      dgates[(size_t)t * k + slot] = v;
-    }
-    // dropped slots
-    const unsigned kept = __reduce_or_sync(0xffffffffu, lane < nk ? 1u << slot : 0u);
-    if (lane < k && !(kept >> lane & 1u)) dgates[(size_t)t * k + lane] = 0.f;
-  }
+  store_dgates<K>(part, red, dgates, in, t, k, W, nk, slot);
 }
 
 // Above 4 slots: the same sums in the same order, but a warp copies its pieces to
@@ -213,25 +221,6 @@ __global__ void __launch_bounds__(256, K <= 2 ? 4 : 3)
 // x 1024 top-8 152 / 158; 64 x 2048 top-6 19.6 / 18.6; but top-3 of 4096 x 1536 62
 // / 59, and top-1 of 4096 x 768 14.4 / 12.3.  With 1 warp a token 92 at 5003 x
 // 2056, with 4 88, with 8 105; 8 pieces deep 86, 4 deep 85.
-
-// The same with one kept slot a lane: lane i < nk holds the i-th one's grouped row,
-// gate and slot number.
-__device__ __forceinline__ int lane_slots(const int32_t* __restrict__ dest,
-                                          const float* __restrict__ gates, int t, int k, int& row,
-                                          float& gate, int& slot) {
-  const int lane = threadIdx.x & 31;
-  int d = -1;
-  float g = 0.f;
-  if (lane < k) {
-    d = __ldg(dest + (size_t)t * k + lane);
-    g = __ldg(gates + (size_t)t * k + lane);
-  }
-  const unsigned kept = __ballot_sync(0xffffffffu, d >= 0);
-  slot = (int)__fns(kept, 0, lane + 1) & 31;
-  row = __shfl_sync(0xffffffffu, d, slot);
-  gate = __shfl_sync(0xffffffffu, g, slot);
-  return __popc(kept);
-}
 
 // A warp's pieces of 32 x 8 columns, in the order: for each of its columns
 // v, v + step, ... (in vectors of 8) the addend's (if there is one), then the nk
@@ -385,24 +374,7 @@ __global__ void __launch_bounds__(256, 3)
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < K; ++j) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
-    if (lane == 0) red[warp][j] = part[j];
-  }
-  if (W > 1) __syncthreads();
-  else __syncwarp();
-  if (in_rows && warp % W == 0) {
-    if (lane < nk) {
-      float v = red[warp][lane];
-      for (int w = 1; w < W; ++w) v += red[warp + w][lane];
-      dgates[(size_t)t * k + slot] = v;
-    }
-    // dropped slots
-    const unsigned kept = __reduce_or_sync(0xffffffffu, lane < nk ? 1u << slot : 0u);
-    if (lane < k && !(kept >> lane & 1u)) dgates[(size_t)t * k + lane] = 0.f;
-  }
+  store_dgates<K>(part, red, dgates, in_rows, t, k, W, nk, slot);
 }
 
 template <typename T>
@@ -413,8 +385,8 @@ cudaError_t run_dropout(const void* x, const void* add, void* out, long long nbl
   T* op = static_cast<T*>(out);
   const unsigned grid = (unsigned)((nblk + 255) / 256);
   if (add != nullptr)
-    return launch_kernel(dropout_kernel<T, 1, true>, grid, 256, 0, s, 0, xp, ap, op, nblk, d);
-  return launch_kernel(dropout_kernel<T, 1, false>, grid, 256, 0, s, 0, xp, ap, op, nblk, d);
+    return launch_kernel(dropout_kernel<T, true>, grid, 256, 0, s, 0, xp, ap, op, nblk, d);
+  return launch_kernel(dropout_kernel<T, false>, grid, 256, 0, s, 0, xp, ap, op, nblk, d);
 }
 
 }  // namespace
