@@ -49,6 +49,9 @@ extern "C" {
  *   losses       (2) fp32 out (0 where nothing is counted)
  *   ws           moe_balance_workspace_size bytes, its own workspace; first
  *                256 bytes as in moe_workspace_init / moe_device_status
+ * A probability whose logit is D below its token's largest is within
+ * 2.3 D + 44 units of 2^-24 of exact, relative (2^x of a rounded product; below
+ * 2^-126 it is 0).
  * Sums over tokens: fp32 for at most 64 tokens (and 8 such sums in pairs up to
  * T = 303103), fp64 above; fixed orders, no floating-point atomics.  T * top_k
  * and n_seqs at most 2^30. */
@@ -162,10 +165,16 @@ int moe_combine_dropout_backward(const moe_config_t* cfg, const moe_dropout_t* d
  *   out, may be dx_add; dA, dB fp32 out, shaped like A and B, every adapter's
  *   written (0 for one without tokens).  base's gradient is dy.
  *   ws: moe_adapter_workspace_size bytes, 256-byte aligned.
- * Tensor cores with fp32 sums; u and v keep fp32 accuracy as operands (split
- * into bf16 terms: where one is infinite its row, and the gradients of its
- * adapter, are NaN).  Fixed orders, no floating-point atomics.  Calls on
- * several streams may share a plan; each needs a workspace of its own. */
+ * Tensor cores with fp32 sums; u and v are fp32 and enter the products as sums
+ * of bf16 terms: two (16 bits) for the bf16 output, three (24 bits) for dx, dA
+ * and dB.  Where one is infinite, or rounds to bf16's infinity, its row and the
+ * gradients of its adapter are NaN.  Fixed orders, no floating-point atomics.
+ * Calls on several streams may share a plan; each needs a workspace of its own.
+ * n_adapters is the number loaded, and every call's cost follows it: the plan
+ * reads token_adapter n_adapters + 1 times from L2 (131072 tokens on 1024
+ * adapters 152 us, on 64 36 us), and the row tiles are chosen as if the tokens
+ * were spread over all of them.  A batch that uses a few of many adapters is
+ * faster on tensors of those alone. */
 size_t moe_adapter_plan_size(const moe_config_t* cfg, int32_t n_adapters);
 int moe_adapter_plan(const moe_config_t* cfg, int32_t n_adapters, const int32_t* token_adapter,
                      void* plan, size_t plan_bytes, moe_stream_t stream);

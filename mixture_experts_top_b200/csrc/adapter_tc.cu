@@ -18,9 +18,11 @@
 // tensor core's own sums truncate), and write D2 through the stage's base tile,
 // so that every global access of a warp covers whole sectors.  u's terms reach
 // the second product before what later launches need is written out.
-// Bound by HBM: 2 (K + 2 N) bytes a row forward, 2 K + 8 N backward.  B200, 8192
-// rows: forward, 4096 wide, rank 16, 44 us (4.6 TB/s); backward, 2048 wide, rank
-// 64, 41 us (4.3 TB/s), where a stage's loads pace the second product.
+// It moves 2 (K + 2 N) bytes a row forward, 2 K + 8 N backward, at two thirds of the
+// measured copy rate: one CTA an SM, so that all read x together, wait while u is
+// formed, and then read and write together.  B200, 8192 rows: forward, 4096 wide, rank
+// 16, 44 us (4.6 TB/s); backward, 2048 wide, rank 64, 41 us (4.3 TB/s), where a
+// stage's loads pace the second product.
 // Every wait is bounded (moe_device.cuh) and recorded on the error word.
 #include "adapter.cuh"
 #include "moe_device.cuh"
