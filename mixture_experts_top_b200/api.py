@@ -432,7 +432,7 @@ def _where(stream):
     import torch
     if not torch.cuda.is_initialized():
         return -2, None
-    dev = torch._C._cuda_getDevice()
+    dev = torch.cuda.current_device()
     return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None
                  else stream.cuda_stream)
 

@@ -32,7 +32,8 @@ def test_size_does_not_follow_the_gradients(moe_lib):
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,d,w,n,r", [
     (64, 264, 136, 300, 16), (3000, 72, 136, 1000, 8), (9000, 40, 72, 3, 8), (9000, 40, 72, 200, 8),
-    (40000, 24, 16, 1, 8), (40000, 24, 16, 37, 16), (6144, 136, 72, 64, 24), (2048, 2048, 512, 8, 96)])
+    (40000, 24, 16, 1, 8), (40000, 24, 16, 37, 16), (6144, 136, 72, 64, 24), (2048, 2048, 512, 8, 96),
+    (3000, 72, 136, 200, 128), (9000, 136, 72, 130, 128)])
 @pytest.mark.parametrize("spread", ["even", "random", "one"])
 def test_parts_stay_inside(T, d, w, n, r, spread):
     g = torch.Generator(device="cuda").manual_seed(T + n)
